@@ -298,6 +298,68 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
                        const float* D, const float* init_states, void* y, float* final_states, int64_t batch,
                        int64_t seqlen, int64_t dim, int64_t dstate, int dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * The gated delta rule: the other recurrence of linear-recurrent sequence layers.  Like the SSD layer
+ * a head keeps a headdim x dstate state that decays by one scalar per token, but a token first takes out
+ * what the state already answers for its key, then writes its value (beta in [0, 1] says how much):
+ *
+ *     S' = exp(g_t) S_{t-1}
+ *     e_t = v_t - S' k_t                  (what the state does not yet answer for k_t)
+ *     S_t = S' + beta_t e_t k_t^T
+ *     y_t = S_t q_t
+ *
+ * v takes the place of x, k of B, q of C in the calls above: k and q are shared by the heads of a group
+ * (head h reads group h / (nheads / ngroups)).  Conventions, limits and errors are those at the top of
+ * this header, and:
+ *   - g is the log decay, <= 0 (dt * A in the SSD layer's terms); it is not clamped, except that
+ *     every g below -1000 acts as -1000 (exp is 0 in fp32 from -104 on), so -inf is a reset.
+ *   - k is used as given.  The recurrence is stable for beta |k|^2 < 2: callers scale k to at most unit
+ *     length.  q carries any scale the caller wants on y.
+ *   - 0 <= batch <= 65535; batch * seqlen (total_tokens) < 2^31; nseq <= 2^24.  There is no chunk size.
+ *   - With bf16 inputs the final states and the fp32 gradients keep fp32's accuracy (about 1e-5 of their
+ *     norm): every fp32 operand of a matrix-core product that reaches them is carried as a pair of bf16
+ *     values.
+ *   - Non-finite inputs: the sums run over blocks of 32 tokens in which a later token's values carry a
+ *     weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of the same
+ *     32-token block of its sequence (and all later ones), never another sequence, batch row or group.
+ * ------------------------------------------------------------------------------------------- */
+
+/* y, final_states of the gated delta rule over whole sequences.
+ *   v T (batch, seqlen, nheads, headdim); g, beta float (batch, seqlen, nheads)
+ *   k, q T (batch, seqlen, ngroups, dstate)
+ *   init_states float (batch, nheads, headdim, dstate) or NULL (zeros)
+ *   y T like v, written; final_states float (batch, nheads, headdim, dstate), written: the state after the
+ *     last token (the initial one when seqlen = 0)
+ *   workspace of at least ssd_delta_forward_workspace_bytes() bytes (0 = the sizes or dtype are refused) */
+size_t ssd_delta_forward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                         int64_t dstate, int64_t ngroups, int dtype);
+int ssd_delta_forward(const void* v, const float* g, const float* beta, const void* k, const void* q,
+                      const float* init_states, void* y, float* final_states, int64_t batch, int64_t seqlen,
+                      int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups, int dtype, void* workspace,
+                      size_t workspace_bytes, void* stream);
+
+/* The same for a packed variable-length batch, laid out as for ssd_forward_varlen: sequence i is tokens
+ * cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of one token axis.
+ *   v, y T (total_tokens, nheads, headdim); g, beta float (total_tokens, nheads); k, q T (total_tokens, ngroups, dstate)
+ *   cu_seqlens int32 (nseq + 1), DEVICE memory, non-decreasing from 0 to total_tokens (empty sequences
+ *     allowed); content not checked, other content yields unspecified values but no access outside the buffers
+ *   init_states float (nseq, nheads, headdim, dstate) or NULL (zeros): a sequence may continue from a state
+ *   final_states float (nseq, nheads, headdim, dstate), written */
+size_t ssd_delta_forward_varlen_workspace_bytes(int64_t total_tokens, int64_t nseq, int64_t nheads, int64_t headdim,
+                                                int64_t dstate, int64_t ngroups, int dtype);
+int ssd_delta_forward_varlen(const void* v, const float* g, const float* beta, const void* k, const void* q,
+                             const int32_t* cu_seqlens, int64_t nseq, const float* init_states, void* y,
+                             float* final_states, int64_t total_tokens, int64_t nheads, int64_t headdim,
+                             int64_t dstate, int64_t ngroups, int dtype, void* workspace, size_t workspace_bytes,
+                             void* stream);
+
+/* One token, the state advanced IN PLACE.
+ *   state float (batch, nheads, headdim, dstate); v T (batch, nheads, headdim); g, beta float (batch, nheads)
+ *   k, q T (batch, ngroups, dstate); y T (batch, nheads, headdim), written */
+int ssd_delta_step(float* state, const void* v, const float* g, const float* beta, const void* k, const void* q,
+                   void* y, int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                   int dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

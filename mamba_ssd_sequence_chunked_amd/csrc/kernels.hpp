@@ -160,4 +160,24 @@ hipError_t launch_backward_f32(const float* x, const float* dt, const float* A, 
                                float* ddt, float* dA, float* dB, float* dC, float* dD, float* dinit, const Dims& d,
                                void* workspace, hipStream_t stream);
 
+// ---- the gated delta rule (the "delta" entry points) -------------------------------------------
+
+// Sizes of one call.  seqs rows of tokens: row s holds tokens [start, end) of one token axis of `tokens`
+// tokens; with cu == nullptr every row has seqlen tokens (start = s * seqlen), else cu (device, seqs + 1
+// offsets) gives them and the kernels clamp what they read from it to [0, tokens].
+struct DeltaDims {
+    int64_t seqs, seqlen, tokens, nheads, headdim, dstate, ngroups;
+    const int32_t* cu;
+};
+
+template <typename T>
+hipError_t launch_delta_step(float* state, const T* v, const float* g, const float* beta, const T* k, const T* q,
+                             T* y, const DeltaDims& d, hipStream_t stream);
+
+template <typename T>
+hipError_t launch_delta_forward(const T* v, const float* g, const float* beta, const T* k, const T* q,
+                                const float* init, T* y, float* final_states, const DeltaDims& d, void* workspace,
+                                hipStream_t stream);
+size_t delta_forward_workspace(const DeltaDims& d, int elem_bytes);
+
 }  // namespace ssd

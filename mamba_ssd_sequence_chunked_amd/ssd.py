@@ -77,6 +77,16 @@ def load_library():
     lib.ssd_backward.argtypes = [vp] * 16 + [i64] * 7 + [i32, vp, sz, vp]
     lib.ssd_selective_scan.restype = i32
     lib.ssd_selective_scan.argtypes = [vp] * 9 + [i64] * 4 + [i32, vp]
+    lib.ssd_delta_forward_workspace_bytes.restype = sz
+    lib.ssd_delta_forward_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_delta_forward.restype = i32
+    lib.ssd_delta_forward.argtypes = [vp] * 8 + [i64] * 6 + [i32, vp, sz, vp]
+    lib.ssd_delta_forward_varlen_workspace_bytes.restype = sz
+    lib.ssd_delta_forward_varlen_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_delta_forward_varlen.restype = i32
+    lib.ssd_delta_forward_varlen.argtypes = [vp] * 6 + [i64] + [vp] * 3 + [i64] * 5 + [i32, vp, sz, vp]
+    lib.ssd_delta_step.restype = i32
+    lib.ssd_delta_step.argtypes = [vp] * 7 + [i64] * 5 + [i32, vp]
     _lib = lib
     return lib
 
@@ -352,6 +362,118 @@ def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
                                 _ptr(y), _ptr(final), b, L, Dm, N, code, _stream(dev))
     _check("ssd_selective_scan", rc)
     return y, final
+
+
+# --- the gated delta rule ----------------------------------------------------------------------
+
+def _on_device(device):
+    """The device the tensors are on made current for the launch, if it is not."""
+    return torch.cuda.device(device)
+
+
+def _delta_need(v, g, beta, k, q, lead, H, P, N, G, dev):
+    _need(v, "v", (*lead, H, P), v.dtype, dev)
+    _need(g, "g", (*lead, H), torch.float32, dev)
+    _need(beta, "beta", (*lead, H), torch.float32, dev)
+    _need(k, "k", (*lead, G, N), v.dtype, dev)
+    _need(q, "q", (*lead, G, N), v.dtype, dev)
+
+
+def delta_forward(v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+                  init_states: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """The gated delta rule over whole sequences: returns (y, final_states); see ssd_delta_forward.
+
+    v (batch, seqlen, nheads, headdim) in bf16 or fp32; g (log decays) and beta (batch, seqlen, nheads)
+    fp32; k, q (batch, seqlen, ngroups, dstate) in v's dtype; init_states (batch, nheads, headdim, dstate)
+    fp32 or None.  A workspace (uint8, ssd_delta_forward_workspace_bytes() long) may be passed in."""
+    lib = load_library()
+    if v.dim() != 4 or k.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, nheads, headdim) and k, q (batch, seqlen, ngroups, dstate)")
+    b, L, H, P = v.shape
+    G, N = k.shape[2], k.shape[3]
+    dev = v.device
+    code = _dtype_code(v)
+    _delta_need(v, g, beta, k, q, (b, L), H, P, N, G, dev)
+    if init_states is not None:
+        _need(init_states, "init_states", (b, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_delta_forward_workspace_bytes(b, L, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_delta_forward_workspace_bytes", -2)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    y = torch.empty_like(v)
+    final = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        rc = lib.ssd_delta_forward(_ptr(v), _ptr(g), _ptr(beta), _ptr(k), _ptr(q), _ptr(init_states), _ptr(y),
+                                   _ptr(final), b, L, H, P, N, G, code, _ptr(workspace), workspace.numel(),
+                                   _stream(dev))
+    _check("ssd_delta_forward", rc)
+    return y, final
+
+
+def delta_forward_varlen(v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+                         cu_seqlens: torch.Tensor, init_states: Optional[torch.Tensor] = None
+                         ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Packed variable-length batch of the gated delta rule; see ssd_delta_forward_varlen.
+
+    v (T, nheads, headdim); g, beta (T, nheads) fp32; k, q (T, ngroups, dstate) in v's dtype; cu_seqlens
+    int32 (nseq + 1,) on the same device; init_states (nseq, nheads, headdim, dstate) fp32 or None.
+    Returns (y in v's dtype, final_states (nseq, nheads, headdim, dstate))."""
+    lib = load_library()
+    if v.dim() != 3 or k.dim() != 3:
+        raise ValueError("v must be (T, nheads, headdim) and k, q (T, ngroups, dstate)")
+    T, H, P = v.shape
+    G, N = k.shape[1], k.shape[2]
+    dev = v.device
+    code = _dtype_code(v)
+    _delta_need(v, g, beta, k, q, (T,), H, P, N, G, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D tensor of nseq + 1 offsets")
+    _need(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, dev)
+    nseq = cu_seqlens.numel() - 1
+    if init_states is not None:
+        _need(init_states, "init_states", (nseq, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_delta_forward_varlen_workspace_bytes(T, nseq, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_delta_forward_varlen_workspace_bytes", -2)
+    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    y = torch.empty_like(v)
+    final = torch.empty((nseq, H, P, N), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        rc = lib.ssd_delta_forward_varlen(_ptr(v), _ptr(g), _ptr(beta), _ptr(k), _ptr(q), _ptr(cu_seqlens), nseq,
+                                          _ptr(init_states), _ptr(y), _ptr(final), T, H, P, N, G, code,
+                                          _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("ssd_delta_forward_varlen", rc)
+    return y, final
+
+
+def delta_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k: torch.Tensor,
+               q: torch.Tensor, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of the gated delta rule: advances ``state`` in place and returns y; see ssd_delta_step.
+
+    state (batch, nheads, headdim, dstate) fp32; v (batch, nheads, headdim) in bf16 or fp32; g, beta
+    (batch, nheads) fp32; k, q (batch, ngroups, dstate) in v's dtype."""
+    lib = load_library()
+    if state.dim() != 4 or k.dim() != 3:
+        raise ValueError("state must be (batch, nheads, headdim, dstate) and k, q (batch, ngroups, dstate)")
+    b, H, P, N = state.shape
+    G = k.shape[1]
+    dev = state.device
+    code = _dtype_code(v)
+    _need(state, "state", (b, H, P, N), torch.float32, dev)
+    _delta_need(v, g, beta, k, q, (b,), H, P, N, G, dev)
+    if y is None:
+        y = torch.empty_like(v)
+    else:
+        _need(y, "y", (b, H, P), v.dtype, dev)
+    with _on_device(dev):
+        rc = lib.ssd_delta_step(_ptr(state), _ptr(v), _ptr(g), _ptr(beta), _ptr(k), _ptr(q), _ptr(y), b, H, P, N, G,
+                                code, _stream(dev))
+    _check("ssd_delta_step", rc)
+    return y
 
 
 # --- the four stages of the chunked mode, one entry point each ---------------------------------
