@@ -1,115 +1,242 @@
-// delta_fwd.hip - the gated delta rule over whole sequences, token by token.
+// delta_fwd.hip - the gated delta rule over whole sequences: the walk over the blocks of 32 tokens.
 //
-//   S' = exp(g_t) S;  e = v_t - S' k_t;  S = S' + beta_t e k_t^T;  y_t = S q_t
+// The rows of the state (head-dimension columns p of v) do not mix, so a wavefront takes 16 of them and keeps
+// its 16 x N piece of the fp32 state in registers for the whole sequence, transposed: accumulator tiles with rows
+// n and columns p.  Two such tiles are an operand fragment as they are (contraction over n), and E, U come out
+// of their products in the same form (rows = tokens, columns p), so a block needs no exchange between
+// lanes or wavefronts:
 //
-// The recurrence as it stands: a workgroup holds one (sequence, head)'s P x N state in registers (a thread
-// owns 4 columns of every (256 / W)-th row) and walks the tokens.
-#include "common.hpp"
-#include "kernels.hpp"
+//   K S^T (rows tokens, columns p) -> E -> e = A E -> U;   Y^T = (S Q^T) diag(gam) + U^T M^T (rows p, columns tokens)
+//   S^T = gam_last S^T + K^T (diag(del) U)
+//
+// For bf16 inputs S, A, E and del U are pairs of bf16 values where they lead to the state (fp32 to about 2^-17);
+// where they lead to y only, which is rounded to bf16 itself, S and U are rounded to bf16 once.
+//
+// A workgroup = NW wavefronts = 16 NW rows of one (sequence, head).  K, Q, the V columns and the block's record come
+// through a ring of NBUF stages of asynchronous global -> LDS copies; one barrier per block.
+#include "delta_tiles.hpp"
 
 namespace ssd {
 
 namespace {
 
-template <typename T, int W, int P>
-__global__ __launch_bounds__(256) void delta_fwd_kernel(
-    const T* __restrict__ v, const float* __restrict__ gv, const float* __restrict__ bv, const T* __restrict__ Km,
-    const T* __restrict__ Qm, const float* __restrict__ init, T* __restrict__ y, float* __restrict__ fin,
-    const int32_t* __restrict__ cu, int64_t seqlen, int64_t tokens, int nheads, int N, int ngroups)
+template <typename T, int NB, int NW>
+struct ChainCfg {
+    static constexpr int kCH = NB * 32 * (int)sizeof(T) / 16;      // chunks of a K or Q row
+    static constexpr int kCV = 16 * NW * (int)sizeof(T) / 16;      // chunks of a V row
+    static constexpr int kK = 0, kQ = DTile<kCH>::kBytes, kV = 2 * DTile<kCH>::kBytes,
+                         kR = kV + DTile<kCV>::kBytes;
+    static constexpr int kStage = kR + DeltaRec<T>::kBytes;
+    static constexpr int kRecInst = (DeltaRec<T>::kBytes + 1023) / 1024;
+    // copies every wavefront makes per stage, at least
+    static constexpr int kMin = 2 * (DTile<kCH>::kInst / NW) + DTile<kCV>::kInst / NW + kRecInst / NW;
+    static constexpr int kBuf = 3 * kStage <= 80 * 1024 ? 3 : 2 * kStage <= 160 * 1024 ? 2 : 1;
+};
+
+template <typename T, int NB, int NW>
+__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
+    const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ init,
+    const unsigned char* __restrict__ recs, T* __restrict__ y, float* __restrict__ fin, DeltaDims d, int nslice)
 {
-    constexpr int kRowsPerPass = 256 / W;
-    constexpr int kPass = (P + kRowsPerPass - 1) / kRowsPerPass;
-    const int64_t sh = blockIdx.x;
-    const int h = (int)(sh % nheads);
-    const int64_t s = sh / nheads;
-    const int grp = h / (nheads / ngroups);
-    const int tid = threadIdx.x;
-    const int col = 4 * (tid % W);
-    const int rsub = tid / W;
-    const bool colok = col < N;
-    int64_t t0 = s * seqlen, t1 = t0 + seqlen;
-    if (cu) {
-        t0 = min(max((int64_t)cu[s], (int64_t)0), tokens);
-        t1 = min(max((int64_t)cu[s + 1], t0), tokens);
-    }
-    float4 st[kPass];
-#pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-        const int p = i * kRowsPerPass + rsub;
-        st[i] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (init && p < P && colok) st[i] = *reinterpret_cast<const float4*>(init + (sh * P + p) * N + col);
-    }
-    for (int64_t t = t0; t < t1; ++t) {
-        const float a = __expf(gv[t * nheads + h]);
-        const float beta = bv[t * nheads + h];
-        float kv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
-        if (colok) {
-            const T* kp = Km + (t * ngroups + grp) * N + col;
-            const T* qp = Qm + (t * ngroups + grp) * N + col;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) { kv[e] = to_f32(kp[e]); qv[e] = to_f32(qp[e]); }
+    using C = ChainCfg<T, NB, NW>;
+    constexpr int kBuf = C::kBuf;
+    static_assert(kBuf >= 2 && kBuf * C::kStage <= 160 * 1024, "ring");
+    __shared__ __attribute__((aligned(1024))) unsigned char ring[kBuf * C::kStage];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int bid = xcd_logical_block(blockIdx.x, gridDim.x);
+    const int slice = bid % nslice;
+    const int64_t sh = bid / nslice;
+    const int h = (int)(sh % d.nheads);
+    const DeltaSeq sq = delta_seq(d, sh / d.nheads);
+    const int grp = h / (int)(d.nheads / d.ngroups);
+    const int N = (int)d.dstate, P = (int)d.headdim;
+    const int pw = 16 * NW * slice;                       // the workgroup's first column of v
+    const int p = pw + 16 * wave + r;                     // this lane's column
+    const int nblk = (sq.len + kDC - 1) / kDC;
+    const int valid = N * (int)sizeof(T) / 16;
+
+    const unsigned krow = (unsigned)(d.ngroups * N * sizeof(T)), vrow = (unsigned)(d.nheads * P * sizeof(T));
+    const T* kbase = Km + (sq.start * d.ngroups + grp) * N;
+    const T* qbase = Qm + (sq.start * d.ngroups + grp) * N;
+    const T* vbase = v + (sq.start * d.nheads + h) * P + pw;
+    T* ybase = y + (sq.start * d.nheads + h) * P + pw + 16 * wave;
+    const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)DeltaRec<T>::kBytes;
+    const unsigned lds0 = lds_addr(&ring[0]);
+
+    if (valid < C::kCH) {
+        // columns past N are never copied: zero them once, so that the state's rows there stay zero
+        for (int i = threadIdx.x; i < kBuf * 32 * C::kCH; i += 64 * NW) {
+            const int row = (i / C::kCH) % 32, b = i / (32 * C::kCH), c = i % C::kCH;
+            if (c >= valid) {
+                unsigned char* st = ring + b * C::kStage + DTile<C::kCH>::offset(row, c);
+                *reinterpret_cast<uint4*>(st + C::kK) = make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(st + C::kQ) = make_uint4(0, 0, 0, 0);
+            }
         }
-        const float kq = group_sum<W>(kv[0] * qv[0] + kv[1] * qv[1] + kv[2] * qv[2] + kv[3] * qv[3]);
-        const T* vr = v + (t * nheads + h) * P;
-        T* yr = y + (t * nheads + h) * P;
+        __syncthreads();
+    }
+
+    auto issue = [&](int c) {
+        const unsigned st = lds0 + (unsigned)(c % kBuf) * C::kStage;
+        const int rmax = min(kDC, sq.len - c * kDC) - 1;
+        const int64_t tok = (int64_t)c * kDC;
+        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(kbase) + tok * krow, krow, rmax, valid,
+                               st + C::kK, wave, lane);
+        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(qbase) + tok * krow, krow, rmax, valid,
+                               st + C::kQ, wave, lane);
+        dtile_copy<C::kCV, NW>(reinterpret_cast<const unsigned char*>(vbase) + tok * vrow, vrow, rmax, C::kCV,
+                               st + C::kV, wave, lane);
+        const unsigned char* rc = rbase + (int64_t)c * d.nheads * DeltaRec<T>::kBytes;
 #pragma unroll
-        for (int i = 0; i < kPass; ++i) {
-            const int p = i * kRowsPerPass + rsub;
-            const bool live = p < P;
-            float4 c = st[i];
-            c.x *= a; c.y *= a; c.z *= a; c.w *= a;
-            const float sk = group_sum<W>(c.x * kv[0] + c.y * kv[1] + c.z * kv[2] + c.w * kv[3]);
-            const float sq = group_sum<W>(c.x * qv[0] + c.y * qv[1] + c.z * qv[2] + c.w * qv[3]);
-            const float u = beta * ((live ? to_f32(vr[p]) : 0.f) - sk);
-            st[i] = make_float4(fmaf(u, kv[0], c.x), fmaf(u, kv[1], c.y), fmaf(u, kv[2], c.z), fmaf(u, kv[3], c.w));
-            if ((tid % W) == 0 && live) yr[p] = from_f32<T>(fmaf(u, kq, sq));
+        for (int q = wave; q < C::kRecInst; q += NW)
+            if (q * 1024 + lane * 16 < DeltaRec<T>::kBytes) dma16_off(rc, q * 1024u + lane * 16u, st + C::kR + q * 1024u);
+    };
+
+    f32x4 S[2 * NB];
+#pragma unroll
+    for (int t = 0; t < 2 * NB; ++t) {
+        S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (init && 16 * t < N) {
+            const float4 a = *reinterpret_cast<const float4*>(init + (sh * P + p) * N + 16 * t + 4 * g);
+            S[t] = f32x4{a.x, a.y, a.z, a.w};
+        }
+    }
+    wait_vmem();          // so that no register load is in flight among the copies that are counted below
+#pragma unroll
+    for (int c = 0; c < kBuf - 1; ++c)
+        if (c < nblk) issue(c);
+
+    for (int c = 0; c < nblk; ++c) {
+        // this stage's copies are done when no more than the later stages' are outstanding
+        constexpr int kLater = (kBuf - 2) * C::kMin < 63 ? (kBuf - 2) * C::kMin : 63;
+        if (c + kBuf - 2 < nblk) wait_vmem_below<kLater>(); else wait_vmem();
+        __syncthreads();                                  // and everybody is done with the stage before it
+        if (c + kBuf - 1 < nblk) issue(c + kBuf - 1);
+        const unsigned char* st = ring + (c % kBuf) * C::kStage;
+        const unsigned char* rec = st + C::kR;
+        const float* tab = reinterpret_cast<const float*>(rec + DeltaRec<T>::kTab);
+        const int rows = min(kDC, sq.len - c * kDC);
+
+        f32x4 ks[2], yt[2];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) ks[t] = yt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int kb = 0; kb < NB; ++kb) {
+            Pair<T> s;
+            const float sv[8] = {S[2 * kb][0], S[2 * kb][1], S[2 * kb][2], S[2 * kb][3],
+                                 S[2 * kb + 1][0], S[2 * kb + 1][1], S[2 * kb + 1][2], S[2 * kb + 1][3]};
+            s.set(sv);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                Vec8<T> kf, qf;
+                dtile_row<C::kCH>(kf, st + C::kK, 16 * t + r, kb, g);
+                mma_xp(ks[t], kf, s);
+                dtile_row<C::kCH>(qf, st + C::kQ, 16 * t + r, kb, g);
+                mma(yt[t], s.hi, qf);
+            }
+        }
+        // E = V - gam K S^T, rows past the sequence zero (their copies repeat the last row)
+        float E[8];
+        {
+            Vec8<T> vf;
+            dtile_col<C::kCV>(vf, st + C::kV, 16 * wave, r, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int row = (i & 3) + 4 * g + (i >> 2) * 16;
+                E[i] = vf.get(i) - tab[row] * ks[i >> 2][i & 3];
+            }
+            if (rows < kDC) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) E[i] = (i & 3) + 4 * g + (i >> 2) * 16 < rows ? E[i] : 0.f;
+            }
+        }
+        Pair<T> ep;
+        ep.set(E);
+        float U[8], dU[8];
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            Pair<T> a;
+            rec_A(a, rec, t, lane);
+            f32x4 e = {0.f, 0.f, 0.f, 0.f};
+            mma_pp(e, a, ep);
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const int row = 16 * t + 4 * g + m;
+                U[4 * t + m] = e[m] * tab[64 + row];
+                dU[4 * t + m] = U[4 * t + m] * tab[32 + row];
+            }
+        }
+        Vec8<T> uf;
+        pack8(uf, U);
+        Pair<T> du;
+        du.set(dU);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const float gam = tab[16 * t + r];
+            yt[t] *= gam;
+            Vec8<T> m;
+            rec_M(m, rec, t, lane);
+            mma(yt[t], uf, m);
+            if (16 * t + r < rows)
+                store4(ybase + (int64_t)(c * kDC + 16 * t + r) * d.nheads * P + 4 * g, yt[t][0], yt[t][1], yt[t][2],
+                       yt[t][3]);
+        }
+        const float gl = tab[31];
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+            S[t] *= gl;
+            Vec8<T> kf;
+            dtile_col<C::kCH>(kf, st + C::kK, 16 * t, r, g);
+            mma_xp(S[t], kf, du);
         }
     }
 #pragma unroll
-    for (int i = 0; i < kPass; ++i) {
-        const int p = i * kRowsPerPass + rsub;
-        if (p < P && colok) *reinterpret_cast<float4*>(fin + (sh * P + p) * N + col) = st[i];
-    }
+    for (int t = 0; t < 2 * NB; ++t)
+        if (16 * t < N) store4(fin + (sh * P + p) * N + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
 }
 
-template <typename T, int W, int P>
-hipError_t launch(const T* v, const float* g, const float* beta, const T* k, const T* q, const float* init, T* y,
-                  float* fin, const DeltaDims& d, hipStream_t stream)
+template <typename T, int NB, int NW>
+hipError_t launch_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
+                        float* fin, const DeltaDims& d, hipStream_t stream)
 {
-    hipLaunchKernelGGL((delta_fwd_kernel<T, W, P>), dim3((unsigned)(d.seqs * d.nheads)), dim3(256), 0, stream, v, g,
-                       beta, k, q, init, y, fin, d.cu, d.seqlen, d.tokens, (int)d.nheads, (int)d.dstate,
-                       (int)d.ngroups);
+    const int nslice = (int)d.headdim / (16 * NW);
+    const int64_t nblocks = d.seqs * d.nheads * nslice;
+    if (nblocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW>), dim3((unsigned)nblocks), dim3(64 * NW), 0, stream, v, k, q,
+                       init, rec, y, fin, d, nslice);
     return hipGetLastError();
 }
 
-template <typename T, int W>
-hipError_t launch_w(const T* v, const float* g, const float* beta, const T* k, const T* q, const float* init, T* y,
-                    float* fin, const DeltaDims& d, hipStream_t stream)
+template <typename T, int NB>
+hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
+                     float* fin, const DeltaDims& d, hipStream_t stream)
 {
-    switch (d.headdim) {
-    case 16: return launch<T, W, 16>(v, g, beta, k, q, init, y, fin, d, stream);
-    case 32: return launch<T, W, 32>(v, g, beta, k, q, init, y, fin, d, stream);
-    case 64: return launch<T, W, 64>(v, g, beta, k, q, init, y, fin, d, stream);
-    case 128: return launch<T, W, 128>(v, g, beta, k, q, init, y, fin, d, stream);
-    default: return hipErrorInvalidValue;
-    }
+    if (d.headdim == 16) return launch_chain<T, NB, 1>(v, k, q, init, rec, y, fin, d, stream);
+    if (d.headdim == 32 || sizeof(T) * NB == 32) return launch_chain<T, NB, 2>(v, k, q, init, rec, y, fin, d, stream);
+    if constexpr (sizeof(T) * NB < 32) return launch_chain<T, NB, 4>(v, k, q, init, rec, y, fin, d, stream);
+    return hipErrorInvalidValue;
 }
 
 }  // namespace
 
-size_t delta_forward_workspace(const DeltaDims&, int) { return 256; }
+size_t delta_forward_workspace(const DeltaDims& d, int elem_bytes)
+{
+    const size_t rec = elem_bytes == 2 ? DeltaRec<bf16>::kBytes : DeltaRec<float>::kBytes;
+    return ((size_t)(delta_slots(d) * d.nheads) * rec + 255) / 256 * 256 + 256;
+}
 
 template <typename T>
 hipError_t launch_delta_forward(const T* v, const float* g, const float* beta, const T* k, const T* q,
-                                const float* init, T* y, float* fin, const DeltaDims& d, void*, hipStream_t stream)
+                                const float* init, T* y, float* fin, const DeltaDims& d, void* workspace,
+                                hipStream_t stream)
 {
-    if (d.seqs == 0) return hipSuccess;
-    const int64_t w = d.dstate / 4;
-    if (w <= 4) return launch_w<T, 4>(v, g, beta, k, q, init, y, fin, d, stream);
-    if (w <= 8) return launch_w<T, 8>(v, g, beta, k, q, init, y, fin, d, stream);
-    if (w <= 16) return launch_w<T, 16>(v, g, beta, k, q, init, y, fin, d, stream);
-    if (w <= 32) return launch_w<T, 32>(v, g, beta, k, q, init, y, fin, d, stream);
-    return launch_w<T, 64>(v, g, beta, k, q, init, y, fin, d, stream);
+    unsigned char* rec = static_cast<unsigned char*>(workspace);
+    hipError_t e = launch_delta_prep<T>(k, q, g, beta, rec, d, stream);
+    if (e != hipSuccess) return e;
+    if (d.dstate <= 32) return launch_nw<T, 1>(v, k, q, init, rec, y, fin, d, stream);
+    if (d.dstate <= 64) return launch_nw<T, 2>(v, k, q, init, rec, y, fin, d, stream);
+    if (d.dstate <= 128) return launch_nw<T, 4>(v, k, q, init, rec, y, fin, d, stream);
+    return launch_nw<T, 8>(v, k, q, init, rec, y, fin, d, stream);
 }
 
 template hipError_t launch_delta_forward<float>(const float*, const float*, const float*, const float*, const float*,

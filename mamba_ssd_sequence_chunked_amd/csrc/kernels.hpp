@@ -174,6 +174,11 @@ template <typename T>
 hipError_t launch_delta_step(float* state, const T* v, const float* g, const float* beta, const T* k, const T* q,
                              T* y, const DeltaDims& d, hipStream_t stream);
 
+// the per-(block, head) records of all blocks (see delta_tiles.hpp)
+template <typename T>
+hipError_t launch_delta_prep(const T* k, const T* q, const float* g, const float* beta, unsigned char* rec,
+                             const DeltaDims& d, hipStream_t stream);
+
 template <typename T>
 hipError_t launch_delta_forward(const T* v, const float* g, const float* beta, const T* k, const T* q,
                                 const float* init, T* y, float* final_states, const DeltaDims& d, void* workspace,
