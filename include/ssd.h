@@ -315,7 +315,8 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *     every g below -1000 acts as -1000 (exp is 0 in fp32 from -104 on), so -inf is a reset.
  *   - k is used as given.  The recurrence is stable for beta |k|^2 < 2: callers scale k to at most unit
  *     length.  q carries any scale the caller wants on y.
- *   - 0 <= batch <= 65535; batch * seqlen (total_tokens) < 2^31; nseq <= 2^24.  There is no chunk size.
+ *   - 0 <= batch <= 65535; nseq <= 2^24; (tokens / 32 + rows) * nheads < 2^24 and rows * nheads * headdim < 2^30,
+ *     rows being batch or nseq (for ssd_delta_step batch * nheads < 2^24).  There is no chunk size.
  *   - With bf16 inputs the final states and the fp32 gradients keep fp32's accuracy (about 1e-5 of their
  *     norm): every fp32 operand of a matrix-core product that reaches them is carried as a pair of bf16
  *     values.
@@ -352,6 +353,21 @@ int ssd_delta_forward_varlen(const void* v, const float* g, const float* beta, c
                              float* final_states, int64_t total_tokens, int64_t nheads, int64_t headdim,
                              int64_t dstate, int64_t ngroups, int dtype, void* workspace, size_t workspace_bytes,
                              void* stream);
+
+/* Gradients of ssd_delta_forward for dL/dy = dy and dL/d(final_states) = dfinal (NULL = 0), by the adjoint of the
+ * recurrence in the same blocks; y and the states are recomputed.
+ *   dy T like v; dfinal float (batch, nheads, headdim, dstate) or NULL
+ *   dv T like v; dg, dbeta float like g; dk, dq T like k (summed over a group's heads, in a fixed order);
+ *   dinit float (batch, nheads, headdim, dstate), written also when init_states is NULL
+ *   workspace of at least ssd_delta_backward_workspace_bytes() bytes
+ * dg at the first token is 0 without an initial state (nothing decays into it). */
+size_t ssd_delta_backward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                          int64_t dstate, int64_t ngroups, int dtype);
+int ssd_delta_backward(const void* v, const float* g, const float* beta, const void* k, const void* q,
+                       const float* init_states, const void* dy, const float* dfinal, void* dv, float* dg,
+                       float* dbeta, void* dk, void* dq, float* dinit, int64_t batch, int64_t seqlen, int64_t nheads,
+                       int64_t headdim, int64_t dstate, int64_t ngroups, int dtype, void* workspace,
+                       size_t workspace_bytes, void* stream);
 
 /* One token, the state advanced IN PLACE.
  *   state float (batch, nheads, headdim, dstate); v T (batch, nheads, headdim); g, beta float (batch, nheads)

@@ -15,8 +15,10 @@ int check_delta(const DeltaDims& d)
     if (rc != SSD_OK) return rc;
     if (d.seqs < 0 || d.seqs > (int64_t(1) << 24) || d.seqlen < 0 || d.tokens < 0) return SSD_ERR_SHAPE;
     if (d.tokens > INT32_MAX) return SSD_ERR_SHAPE;                      // cu_seqlens holds 32-bit offsets
-    // one workgroup per (32-token chunk or row, head, slice of the head dimension) in a one-dimensional grid
-    if ((d.tokens / 32 + d.seqs) * d.nheads * 8 > INT32_MAX) return SSD_ERR_SHAPE;
+    // one-dimensional grids of fewer than 2^32 threads: 256 a (block of 32 tokens, head), 64 a (row, head, 16 of
+    // the head dimension)
+    if ((d.tokens / 32 + d.seqs) * d.nheads >= (int64_t(1) << 24)) return SSD_ERR_SHAPE;
+    if (d.seqs * d.nheads * d.headdim >= (int64_t(1) << 30)) return SSD_ERR_SHAPE;
     if (d.tokens * d.nheads * (d.headdim > d.dstate ? d.headdim : d.dstate) > (int64_t(1) << 40)) return SSD_ERR_SHAPE;
     if (d.seqs * d.nheads * d.headdim * d.dstate > (int64_t(1) << 40)) return SSD_ERR_SHAPE;
     return SSD_OK;
@@ -111,6 +113,51 @@ int ssd_delta_forward_varlen(const void* v, const float* g, const float* beta, c
                               stream);
 }
 
+size_t ssd_delta_backward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                          int64_t dstate, int64_t ngroups, int dtype)
+{
+    const DeltaDims d = batch_dims(batch, seqlen, nheads, headdim, dstate, ngroups);
+    if (!valid_dtype(dtype) || check_delta(d) != SSD_OK) return 0;
+    return delta_backward_workspace(d, (int)elem_size(dtype));
+}
+
+int ssd_delta_backward(const void* v, const float* g, const float* beta, const void* k, const void* q,
+                       const float* init_states, const void* dy, const float* dfinal, void* dv, float* dg,
+                       float* dbeta, void* dk, void* dq, float* dinit, int64_t batch, int64_t seqlen, int64_t nheads,
+                       int64_t headdim, int64_t dstate, int64_t ngroups, int dtype, void* workspace,
+                       size_t workspace_bytes, void* stream)
+{
+    const DeltaDims d = batch_dims(batch, seqlen, nheads, headdim, dstate, ngroups);
+    if (!valid_dtype(dtype)) return SSD_ERR_DTYPE;
+    int rc = check_delta(d);
+    if (rc != SSD_OK) return rc;
+    if (batch == 0) return SSD_OK;
+    if (!dinit) return SSD_ERR_NULL;
+    if (seqlen > 0 && (!v || !g || !beta || !k || !q || !dy || !dv || !dg || !dbeta || !dk || !dq)) return SSD_ERR_NULL;
+    const size_t es = elem_size(dtype);
+    const size_t need = delta_backward_workspace(d, (int)es);
+    if (workspace_bytes < need) return SSD_ERR_WORKSPACE;
+    if (!workspace) return SSD_ERR_NULL;
+    if (!aligned16(workspace) || !aligned16(v) || !aligned16(k) || !aligned16(q) || !aligned16(dy) || !aligned16(dv) ||
+        !aligned16(dk) || !aligned16(dq) || !aligned16(init_states) || !aligned16(dfinal) || !aligned16(dinit))
+        return SSD_ERR_SHAPE;
+    const size_t nv = (size_t)(d.tokens * nheads * headdim) * es;
+    const size_t nk = (size_t)(d.tokens * ngroups * dstate) * es;
+    const size_t ng = (size_t)(d.tokens * nheads) * 4;
+    const size_t nst = (size_t)(batch * nheads * headdim * dstate) * 4;
+    if (any_overlap({{dv, nv}, {dg, ng}, {dbeta, ng}, {dk, nk}, {dq, nk}, {dinit, nst}, {workspace, need}},
+                    {{v, nv}, {g, ng}, {beta, ng}, {k, nk}, {q, nk}, {init_states, nst}, {dy, nv}, {dfinal, nst}}))
+        return SSD_ERR_ALIAS;
+    hipStream_t s = (hipStream_t)stream;
+    if (dtype == SSD_BF16)
+        return hip_status(launch_delta_backward<bf16>((const bf16*)v, g, beta, (const bf16*)k, (const bf16*)q,
+                                                      init_states, (const bf16*)dy, dfinal, (bf16*)dv, dg, dbeta,
+                                                      (bf16*)dk, (bf16*)dq, dinit, d, workspace, s));
+    return hip_status(launch_delta_backward<float>((const float*)v, g, beta, (const float*)k, (const float*)q,
+                                                   init_states, (const float*)dy, dfinal, (float*)dv, dg, dbeta,
+                                                   (float*)dk, (float*)dq, dinit, d, workspace, s));
+}
+
 int ssd_delta_step(float* state, const void* v, const float* g, const float* beta, const void* k, const void* q,
                    void* y, int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
                    int dtype, void* stream)
@@ -118,7 +165,7 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
     if (!valid_dtype(dtype)) return SSD_ERR_DTYPE;
     int rc = check_common(batch, nheads, headdim, dstate, ngroups);
     if (rc != SSD_OK) return rc;
-    if (batch * nheads > INT32_MAX) return SSD_ERR_SHAPE;
+    if (batch * nheads >= (int64_t(1) << 24)) return SSD_ERR_SHAPE;      // a grid of fewer than 2^32 threads
     if (batch == 0) return SSD_OK;
     if (!state || !v || !g || !beta || !k || !q || !y) return SSD_ERR_NULL;
     if (!aligned16(state)) return SSD_ERR_SHAPE;

@@ -12,6 +12,9 @@
 // For bf16 inputs S, A, E and del U are pairs of bf16 values where they lead to the state (fp32 to about 2^-17);
 // where they lead to y only, which is rounded to bf16 itself, S and U are rounded to bf16 once.
 //
+// kBwd is the backward's walk forward: the same block by block, with y kept to fp32's accuracy (pairs there too)
+// and, in place of y and the final state, what the walk back and the gradients of k and q need (DeltaKeep).
+//
 // A workgroup = NW wavefronts = 16 NW rows of one (sequence, head).  K, Q, the V columns and the block's record come
 // through a ring of NBUF stages of asynchronous global -> LDS copies; one barrier per block.
 #include "delta_tiles.hpp"
@@ -20,25 +23,28 @@ namespace ssd {
 
 namespace {
 
-template <typename T, int NB, int NW>
+template <typename T, int NB, int NW, bool kBwd>
 struct ChainCfg {
+    using R = DeltaRec<T, kBwd>;
     static constexpr int kCH = NB * 32 * (int)sizeof(T) / 16;      // chunks of a K or Q row
     static constexpr int kCV = 16 * NW * (int)sizeof(T) / 16;      // chunks of a V row
     static constexpr int kK = 0, kQ = DTile<kCH>::kBytes, kV = 2 * DTile<kCH>::kBytes,
                          kR = kV + DTile<kCV>::kBytes;
-    static constexpr int kStage = kR + DeltaRec<T>::kBytes;
-    static constexpr int kRecInst = (DeltaRec<T>::kBytes + 1023) / 1024;
+    static constexpr int kStage = kR + R::kFwdBytes;
+    static constexpr int kRecInst = (R::kFwdBytes + 1023) / 1024;
     // copies every wavefront makes per stage, at least
     static constexpr int kMin = 2 * (DTile<kCH>::kInst / NW) + DTile<kCV>::kInst / NW + kRecInst / NW;
     static constexpr int kBuf = 3 * kStage <= 80 * 1024 ? 3 : 2 * kStage <= 160 * 1024 ? 2 : 1;
 };
 
-template <typename T, int NB, int NW>
+template <typename T, int NB, int NW, bool kBwd>
 __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ init,
-    const unsigned char* __restrict__ recs, T* __restrict__ y, float* __restrict__ fin, DeltaDims d, int nslice)
+    const unsigned char* __restrict__ recs, T* __restrict__ y, float* __restrict__ fin, DeltaKeep<T> keep, DeltaDims d,
+    int nslice)
 {
-    using C = ChainCfg<T, NB, NW>;
+    using C = ChainCfg<T, NB, NW, kBwd>;
+    using R = DeltaRec<T, kBwd>;
     constexpr int kBuf = C::kBuf;
     static_assert(kBuf >= 2 && kBuf * C::kStage <= 160 * 1024, "ring");
     __shared__ __attribute__((aligned(1024))) unsigned char ring[kBuf * C::kStage];
@@ -60,7 +66,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     const T* qbase = Qm + (sq.start * d.ngroups + grp) * N;
     const T* vbase = v + (sq.start * d.nheads + h) * P + pw;
     T* ybase = y + (sq.start * d.nheads + h) * P + pw + 16 * wave;
-    const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)DeltaRec<T>::kBytes;
+    const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)R::kBytes;
     const unsigned lds0 = lds_addr(&ring[0]);
 
     if (valid < C::kCH) {
@@ -86,10 +92,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
                                st + C::kQ, wave, lane);
         dtile_copy<C::kCV, NW>(reinterpret_cast<const unsigned char*>(vbase) + tok * vrow, vrow, rmax, C::kCV,
                                st + C::kV, wave, lane);
-        const unsigned char* rc = rbase + (int64_t)c * d.nheads * DeltaRec<T>::kBytes;
-#pragma unroll
-        for (int q = wave; q < C::kRecInst; q += NW)
-            if (q * 1024 + lane * 16 < DeltaRec<T>::kBytes) dma16_off(rc, q * 1024u + lane * 16u, st + C::kR + q * 1024u);
+        linear_copy<R::kFwdBytes, NW>(rbase + (int64_t)c * d.nheads * R::kBytes, st + C::kR, wave, lane);
     };
 
     f32x4 S[2 * NB];
@@ -106,15 +109,41 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     for (int c = 0; c < kBuf - 1; ++c)
         if (c < nblk) issue(c);
 
+    // the state entering a chunk of 64 tokens (k = 0 ..) and after the last one
+    auto keep_state = [&](int k) {
+        const int64_t at = (((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
+#pragma unroll
+        for (int t = 0; t < 2 * NB; ++t) {
+            if (16 * t < N) {
+                store4(keep.S + at + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
+                if (sizeof(T) == 2) {
+                    float lo[4];
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) lo[m] = S[t][m] - to_f32(from_f32<T>(S[t][m]));
+                    store4(keep.Slo + at + 16 * t + 4 * g, lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+        }
+    };
+
     for (int c = 0; c < nblk; ++c) {
         // this stage's copies are done when no more than the later stages' are outstanding
         constexpr int kLater = (kBuf - 2) * C::kMin < 63 ? (kBuf - 2) * C::kMin : 63;
         if (c + kBuf - 2 < nblk) wait_vmem_below<kLater>(); else wait_vmem();
         __syncthreads();                                  // and everybody is done with the stage before it
+        float4 dyv[2];
+        if constexpr (kBwd) {
+            if (c % 2 == 0) keep_state(c / 2);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int64_t tok = sq.start + min(c * kDC + 16 * t + r, sq.len - 1);
+                dyv[t] = load4f(keep.dy + (tok * d.nheads + h) * P + pw + 16 * wave + 4 * g);
+            }
+        }
         if (c + kBuf - 1 < nblk) issue(c + kBuf - 1);
         const unsigned char* st = ring + (c % kBuf) * C::kStage;
         const unsigned char* rec = st + C::kR;
-        const float* tab = reinterpret_cast<const float*>(rec + DeltaRec<T>::kTab);
+        const float* tab = reinterpret_cast<const float*>(rec + R::kTab);
         const int rows = min(kDC, sq.len - c * kDC);
 
         f32x4 ks[2], yt[2];
@@ -132,7 +161,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
                 dtile_row<C::kCH>(kf, st + C::kK, 16 * t + r, kb, g);
                 mma_xp(ks[t], kf, s);
                 dtile_row<C::kCH>(qf, st + C::kQ, 16 * t + r, kb, g);
-                mma(yt[t], s.hi, qf);
+                if constexpr (kBwd) mma_px(yt[t], s, qf); else mma(yt[t], s.hi, qf);
             }
         }
         // E = V - gam K S^T, rows past the sequence zero (their copies repeat the last row)
@@ -156,7 +185,7 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             Pair<T> a;
-            rec_A(a, rec, t, lane);
+            rec_rows(a, rec + R::kA, t, r, g);
             f32x4 e = {0.f, 0.f, 0.f, 0.f};
             mma_pp(e, a, ep);
 #pragma unroll
@@ -165,21 +194,43 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
                 U[4 * t + m] = e[m] * tab[64 + row];
                 dU[4 * t + m] = U[4 * t + m] * tab[32 + row];
             }
+            if constexpr (kBwd) {
+                // e once more with columns = tokens, the form in which it is kept
+                f32x4 et = {0.f, 0.f, 0.f, 0.f};
+                mma_pp(et, ep, a);
+                store4(keep.e + keep.frag(sq.slot + c, h, pw / 16 + wave, d) + t * 256 + lane * 4, et[0], et[1], et[2], et[3]);
+            }
         }
-        Vec8<T> uf;
-        pack8(uf, U);
         Pair<T> du;
         du.set(dU);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            const float gam = tab[16 * t + r];
-            yt[t] *= gam;
-            Vec8<T> m;
-            rec_M(m, rec, t, lane);
-            mma(yt[t], uf, m);
-            if (16 * t + r < rows)
-                store4(ybase + (int64_t)(c * kDC + 16 * t + r) * d.nheads * P + 4 * g, yt[t][0], yt[t][1], yt[t][2],
-                       yt[t][3]);
+        for (int t = 0; t < 2; ++t) yt[t] *= tab[16 * t + r];
+        if constexpr (kBwd) {
+            Pair<T> up;
+            up.set(U);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                Pair<T> m;
+                rec_rows(m, rec + R::kM, t, r, g);
+                mma_pp(yt[t], up, m);
+                float dot = yt[t][0] * dyv[t].x + yt[t][1] * dyv[t].y + yt[t][2] * dyv[t].z + yt[t][3] * dyv[t].w;
+                dot += __shfl_xor(dot, 16, kWave);
+                dot += __shfl_xor(dot, 32, kWave);
+                if (g == 0 && 16 * t + r < rows)
+                    keep.ydy[(pw / 16 + wave) * d.tokens * d.nheads + (sq.start + c * kDC + 16 * t + r) * d.nheads + h] = dot;
+            }
+        } else {
+            Vec8<T> uf;
+            pack8(uf, U);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                Vec8<T> m;
+                dtile_row<kRecCH<T>>(m, rec + R::kM, 16 * t + r, 0, g);
+                mma(yt[t], uf, m);
+                if (16 * t + r < rows)
+                    store4(ybase + (int64_t)(c * kDC + 16 * t + r) * d.nheads * P + 4 * g, yt[t][0], yt[t][1],
+                           yt[t][2], yt[t][3]);
+            }
         }
         const float gl = tab[31];
 #pragma unroll
@@ -190,30 +241,36 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
             mma_xp(S[t], kf, du);
         }
     }
+    if constexpr (kBwd) {
+        keep_state((int)keep.chunks);
+    } else {
 #pragma unroll
-    for (int t = 0; t < 2 * NB; ++t)
-        if (16 * t < N) store4(fin + (sh * P + p) * N + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
+        for (int t = 0; t < 2 * NB; ++t)
+            if (16 * t < N) store4(fin + (sh * P + p) * N + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
+    }
 }
 
-template <typename T, int NB, int NW>
+template <typename T, int NB, int NW, bool kBwd>
 hipError_t launch_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
-                        float* fin, const DeltaDims& d, hipStream_t stream)
+                        float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream)
 {
     const int nslice = (int)d.headdim / (16 * NW);
     const int64_t nblocks = d.seqs * d.nheads * nslice;
     if (nblocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW>), dim3((unsigned)nblocks), dim3(64 * NW), 0, stream, v, k, q,
-                       init, rec, y, fin, d, nslice);
+    hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), 0, stream, v, k,
+                       q, init, rec, y, fin, keep, d, nslice);
     return hipGetLastError();
 }
 
-template <typename T, int NB>
+template <typename T, int NB, bool kBwd>
 hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
-                     float* fin, const DeltaDims& d, hipStream_t stream)
+                     float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream)
 {
-    if (d.headdim == 16) return launch_chain<T, NB, 1>(v, k, q, init, rec, y, fin, d, stream);
-    if (d.headdim == 32 || sizeof(T) * NB == 32) return launch_chain<T, NB, 2>(v, k, q, init, rec, y, fin, d, stream);
-    if constexpr (sizeof(T) * NB < 32) return launch_chain<T, NB, 4>(v, k, q, init, rec, y, fin, d, stream);
+    if (d.headdim == 16) return launch_chain<T, NB, 1, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    // two stages of the widest fp32 rows leave room for two wavefronts' columns
+    if (d.headdim == 32 || sizeof(T) * NB == 32)
+        return launch_chain<T, NB, 2, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    if constexpr (sizeof(T) * NB < 32) return launch_chain<T, NB, 4, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
     return hipErrorInvalidValue;
 }
 
@@ -221,8 +278,18 @@ hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, cons
 
 size_t delta_forward_workspace(const DeltaDims& d, int elem_bytes)
 {
-    const size_t rec = elem_bytes == 2 ? DeltaRec<bf16>::kBytes : DeltaRec<float>::kBytes;
+    const size_t rec = elem_bytes == 2 ? DeltaRec<bf16, false>::kBytes : DeltaRec<float, false>::kBytes;
     return ((size_t)(delta_slots(d) * d.nheads) * rec + 255) / 256 * 256 + 256;
+}
+
+template <typename T, bool kBwd>
+hipError_t launch_delta_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
+                              float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream)
+{
+    if (d.dstate <= 32) return launch_nw<T, 1, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    if (d.dstate <= 64) return launch_nw<T, 2, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    if (d.dstate <= 128) return launch_nw<T, 4, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    return launch_nw<T, 8, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
 }
 
 template <typename T>
@@ -231,17 +298,19 @@ hipError_t launch_delta_forward(const T* v, const float* g, const float* beta, c
                                 hipStream_t stream)
 {
     unsigned char* rec = static_cast<unsigned char*>(workspace);
-    hipError_t e = launch_delta_prep<T>(k, q, g, beta, rec, d, stream);
+    hipError_t e = launch_delta_prep<T, false>(k, q, g, beta, rec, d, stream);
     if (e != hipSuccess) return e;
-    if (d.dstate <= 32) return launch_nw<T, 1>(v, k, q, init, rec, y, fin, d, stream);
-    if (d.dstate <= 64) return launch_nw<T, 2>(v, k, q, init, rec, y, fin, d, stream);
-    if (d.dstate <= 128) return launch_nw<T, 4>(v, k, q, init, rec, y, fin, d, stream);
-    return launch_nw<T, 8>(v, k, q, init, rec, y, fin, d, stream);
+    return launch_delta_chain<T, false>(v, k, q, init, rec, y, fin, DeltaKeep<T>{}, d, stream);
 }
 
-template hipError_t launch_delta_forward<float>(const float*, const float*, const float*, const float*, const float*,
-                                                const float*, float*, float*, const DeltaDims&, void*, hipStream_t);
-template hipError_t launch_delta_forward<bf16>(const bf16*, const float*, const float*, const bf16*, const bf16*,
-                                               const float*, bf16*, float*, const DeltaDims&, void*, hipStream_t);
+#define SSD_DELTA_FWD(T)                                                                                             \
+    template hipError_t launch_delta_forward<T>(const T*, const float*, const float*, const T*, const T*,            \
+                                                const float*, T*, float*, const DeltaDims&, void*, hipStream_t);     \
+    template hipError_t launch_delta_chain<T, true>(const T*, const T*, const T*, const float*,                      \
+                                                    const unsigned char*, T*, float*, const DeltaKeep<T>&,           \
+                                                    const DeltaDims&, hipStream_t);
+SSD_DELTA_FWD(float)
+SSD_DELTA_FWD(bf16)
+#undef SSD_DELTA_FWD
 
 }  // namespace ssd

@@ -74,13 +74,20 @@ __device__ __forceinline__ bool delta_slot(const DeltaDims& d, int64_t slot, Del
 
 // ---- records --------------------------------------------------------------------------------------------
 
-// A and M as operand fragments of two row tiles (rows 16 t + r) with slots over the 32 columns, 16 bytes a lane:
-// bf16 inputs: A as a pair (hi, lo planes), M rounded; fp32 inputs: two planes (slots 0-3, 4-7) each of A and M.
-// Then the tables gam, del, beta (32 floats each).
-template <typename T> struct DeltaRec {
-    static constexpr int kPlanes = sizeof(T) == 2 ? 3 : 4;      // planes of 2 tiles x 64 lanes x 16 bytes
-    static constexpr int kTab = kPlanes * 2048;
-    static constexpr int kBytes = kTab + 512;
+// What delta_prep leaves for a block and head: 32 x 32 matrices in T as LDS tiles (DTile, so that they can be read
+// by rows and by columns), bf16 ones as a hi and a lo plane, and the tables gam, del, beta (32 floats each).
+//   forward:  A (hi, lo), M (hi only), tables
+//   backward: A, M (both as pairs), tables, B = (I + diag(beta) X)^-1 (pair); the walk forward reads A to the tables,
+//             the walk back M to B
+template <typename T, bool kBwd> struct DeltaRec {
+    static constexpr int kPair = sizeof(T) == 2 ? 2 : 1;
+    static constexpr int kMat = 32 * 32 * (int)sizeof(T);
+    static constexpr int kA = 0, kM = kPair * kMat;
+    static constexpr int kTab = kM + (kBwd ? kPair : 1) * kMat;
+    static constexpr int kB = kTab + 512;
+    static constexpr int kBytes = kB + (kBwd ? kPair * kMat : 0);
+    static constexpr int kFwdBytes = kB;               // what the walk forward reads, from the record's start
+    static constexpr int kRevBytes = kBytes - kM;      // what the walk back reads, from kM on
 };
 
 // ---- LDS tiles ------------------------------------------------------------------------------------------
@@ -170,7 +177,9 @@ template <> struct Pair<float> {
     Vec8<float> hi;
     __device__ __forceinline__ void set(const float (&v)[8]) { pack8(hi, v); }
 };
-// a exact, b a pair (either order of the operands); both pairs: without the product of the two low parts (2^-18)
+// a exact, b a pair and the other way round; both pairs: without the product of the two low parts (2^-18)
+__device__ __forceinline__ void mma_px(f32x4& acc, const Pair<bf16>& a, const Vec8<bf16>& b) { mma(acc, a.lo, b); mma(acc, a.hi, b); }
+__device__ __forceinline__ void mma_px(f32x4& acc, const Pair<float>& a, const Vec8<float>& b) { mma(acc, a.hi, b); }
 __device__ __forceinline__ void mma_xp(f32x4& acc, const Vec8<bf16>& a, const Pair<bf16>& b) { mma(acc, a, b.lo); mma(acc, a, b.hi); }
 __device__ __forceinline__ void mma_xp(f32x4& acc, const Vec8<float>& a, const Pair<float>& b) { mma(acc, a, b.hi); }
 __device__ __forceinline__ void mma_pp(f32x4& acc, const Pair<bf16>& a, const Pair<bf16>& b)
@@ -181,24 +190,55 @@ __device__ __forceinline__ void mma_pp(f32x4& acc, const Pair<bf16>& a, const Pa
 }
 __device__ __forceinline__ void mma_pp(f32x4& acc, const Pair<float>& a, const Pair<float>& b) { mma(acc, a.hi, b.hi); }
 
-// A fragment of a record: row tile t of A (as a pair) or M.
-__device__ __forceinline__ void rec_A(Pair<bf16>& f, const unsigned char* rec, int t, int lane)
+// The matrices of a record: CH of their tiles, and fragments by rows (row tile t) and by columns (column tile t).
+template <typename T> constexpr int kRecCH = 32 * (int)sizeof(T) / 16;
+__device__ __forceinline__ void rec_rows(Pair<bf16>& f, const unsigned char* m, int t, int r, int g)
 {
-    f.hi.v = *reinterpret_cast<const bf16x8*>(rec + t * 1024 + lane * 16);
-    f.lo.v = *reinterpret_cast<const bf16x8*>(rec + 2048 + t * 1024 + lane * 16);
+    dtile_row<4>(f.hi, m, 16 * t + r, 0, g);
+    dtile_row<4>(f.lo, m + 2048, 16 * t + r, 0, g);
 }
-__device__ __forceinline__ void rec_M(Vec8<bf16>& f, const unsigned char* rec, int t, int lane)
+__device__ __forceinline__ void rec_rows(Pair<float>& f, const unsigned char* m, int t, int r, int g)
 {
-    f.v = *reinterpret_cast<const bf16x8*>(rec + 4096 + t * 1024 + lane * 16);
+    dtile_row<8>(f.hi, m, 16 * t + r, 0, g);
 }
-__device__ __forceinline__ void rec_f32(Vec8<float>& f, const unsigned char* plane, int t, int lane)
+__device__ __forceinline__ void rec_cols(Pair<bf16>& f, const unsigned char* m, int t, int r, int g)
 {
-    const float4 a = *reinterpret_cast<const float4*>(plane + t * 1024 + lane * 16);
-    const float4 b = *reinterpret_cast<const float4*>(plane + 2048 + t * 1024 + lane * 16);
-    f.v[0] = a.x; f.v[1] = a.y; f.v[2] = a.z; f.v[3] = a.w;
-    f.v[4] = b.x; f.v[5] = b.y; f.v[6] = b.z; f.v[7] = b.w;
+    dtile_col<4>(f.hi, m, 16 * t, r, g);
+    dtile_col<4>(f.lo, m + 2048, 16 * t, r, g);
 }
-__device__ __forceinline__ void rec_A(Pair<float>& f, const unsigned char* rec, int t, int lane) { rec_f32(f.hi, rec, t, lane); }
-__device__ __forceinline__ void rec_M(Vec8<float>& f, const unsigned char* rec, int t, int lane) { rec_f32(f, rec + 4096, t, lane); }
+__device__ __forceinline__ void rec_cols(Pair<float>& f, const unsigned char* m, int t, int r, int g)
+{
+    dtile_col<8>(f.hi, m, 16 * t, r, g);
+}
+
+// Start this wavefront's share of the copy of `bytes` consecutive bytes (a multiple of 16).
+template <int BYTES, int NW>
+__device__ __forceinline__ void linear_copy(const unsigned char* src, unsigned lds, int wave, int lane)
+{
+#pragma unroll
+    for (int k = 0; k < ((BYTES + 1023) / 1024 + NW - 1) / NW; ++k) {
+        const int q = wave + NW * k;
+        if (q * 1024 + lane * 16 < BYTES) dma16_off(src, q * 1024u + lane * 16u, lds + q * 1024u);
+    }
+}
+
+// ---- what the backward's walk forward keeps -------------------------------------------------------------
+
+template <typename T> struct DeltaKeep {
+    const T* dy;
+    float* e;                // e of every block, head and 16 columns: 2 token tiles x 64 lanes x 4 columns (frag)
+    float* ydy;              // (headdim / 16, tokens, nheads): dy . y over 16 columns
+    T* S;                    // (seqs, chunks + 1, nheads, headdim, dstate): the state entering each 64-token chunk,
+    T* Slo;                  //   and after the last; for bf16 also what the rounding to T drops
+    int64_t chunks;          // 64-token chunks of a row
+    __device__ __forceinline__ int64_t frag(int64_t slot, int h, int pt, const DeltaDims& d) const
+    {
+        return ((slot * d.nheads + h) * (d.headdim / 16) + pt) * 512;
+    }
+};
+
+template <typename T, bool kBwd>
+hipError_t launch_delta_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
+                              float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream);
 
 }  // namespace ssd

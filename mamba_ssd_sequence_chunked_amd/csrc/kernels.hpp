@@ -175,7 +175,7 @@ hipError_t launch_delta_step(float* state, const T* v, const float* g, const flo
                              T* y, const DeltaDims& d, hipStream_t stream);
 
 // the per-(block, head) records of all blocks (see delta_tiles.hpp)
-template <typename T>
+template <typename T, bool kBwd>
 hipError_t launch_delta_prep(const T* k, const T* q, const float* g, const float* beta, unsigned char* rec,
                              const DeltaDims& d, hipStream_t stream);
 
@@ -184,5 +184,11 @@ hipError_t launch_delta_forward(const T* v, const float* g, const float* beta, c
                                 const float* init, T* y, float* final_states, const DeltaDims& d, void* workspace,
                                 hipStream_t stream);
 size_t delta_forward_workspace(const DeltaDims& d, int elem_bytes);
+
+template <typename T>
+hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, const T* k, const T* q,
+                                 const float* init, const T* dy, const float* dfinal, T* dv, float* dg, float* dbeta,
+                                 T* dk, T* dq, float* dinit, const DeltaDims& d, void* workspace, hipStream_t stream);
+size_t delta_backward_workspace(const DeltaDims& d, int elem_bytes);
 
 }  // namespace ssd

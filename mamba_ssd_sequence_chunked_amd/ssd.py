@@ -85,6 +85,10 @@ def load_library():
     lib.ssd_delta_forward_varlen_workspace_bytes.argtypes = [i64] * 6 + [i32]
     lib.ssd_delta_forward_varlen.restype = i32
     lib.ssd_delta_forward_varlen.argtypes = [vp] * 6 + [i64] + [vp] * 3 + [i64] * 5 + [i32, vp, sz, vp]
+    lib.ssd_delta_backward_workspace_bytes.restype = sz
+    lib.ssd_delta_backward_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_delta_backward.restype = i32
+    lib.ssd_delta_backward.argtypes = [vp] * 14 + [i64] * 6 + [i32, vp, sz, vp]
     lib.ssd_delta_step.restype = i32
     lib.ssd_delta_step.argtypes = [vp] * 7 + [i64] * 5 + [i32, vp]
     _lib = lib
@@ -448,6 +452,39 @@ def delta_forward_varlen(v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k
                                           _ptr(workspace), workspace.numel(), _stream(dev))
     _check("ssd_delta_forward_varlen", rc)
     return y, final
+
+
+def delta_backward(v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+                   dy: torch.Tensor, init_states: Optional[torch.Tensor] = None,
+                   dfinal: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``delta_forward`` for dL/dy = dy and dL/d(final_states) = dfinal (None = 0); see
+    ssd_delta_backward.  Returns a dict with dv, dg, dbeta, dk, dq, dinit (dv, dk, dq in v's dtype)."""
+    lib = load_library()
+    if v.dim() != 4 or k.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, nheads, headdim) and k, q (batch, seqlen, ngroups, dstate)")
+    b, L, H, P = v.shape
+    G, N = k.shape[2], k.shape[3]
+    dev = v.device
+    code = _dtype_code(v)
+    _delta_need(v, g, beta, k, q, (b, L), H, P, N, G, dev)
+    _need(dy, "dy", (b, L, H, P), v.dtype, dev)
+    if init_states is not None:
+        _need(init_states, "init_states", (b, H, P, N), torch.float32, dev)
+    if dfinal is not None:
+        _need(dfinal, "dfinal", (b, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_delta_backward_workspace_bytes(b, L, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_delta_backward_workspace_bytes", -2)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    out = dict(dv=torch.empty_like(v), dg=torch.empty_like(g), dbeta=torch.empty_like(beta), dk=torch.empty_like(k),
+               dq=torch.empty_like(q), dinit=torch.empty((b, H, P, N), dtype=torch.float32, device=dev))
+    with _on_device(dev):
+        rc = lib.ssd_delta_backward(_ptr(v), _ptr(g), _ptr(beta), _ptr(k), _ptr(q), _ptr(init_states), _ptr(dy),
+                                    _ptr(dfinal), _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dbeta"]),
+                                    _ptr(out["dk"]), _ptr(out["dq"]), _ptr(out["dinit"]), b, L, H, P, N, G, code,
+                                    _ptr(ws), ws.numel(), _stream(dev))
+    _check("ssd_delta_backward", rc)
+    return out
 
 
 def delta_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torch.Tensor, k: torch.Tensor,

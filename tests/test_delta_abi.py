@@ -34,6 +34,7 @@ def forward(**kw):
 @pytest.mark.parametrize("kw,code", SIZES + [
     (dict(L=-1), ERR_SHAPE), (dict(b=-1), ERR_SHAPE), (dict(b=65536), ERR_SHAPE),
     (dict(b=2, L=1 << 30), ERR_SHAPE),                    # 2^31 tokens
+    (dict(b=1, L=1 << 27), ERR_SHAPE),                    # 2^24 blocks of 32 tokens x heads
     (dict(b=60000, L=(1 << 62)), ERR_SHAPE),              # the product would overflow
     (dict(v=None), ERR_NULL), (dict(g=None), ERR_NULL), (dict(fin=None), ERR_NULL), (dict(ws=None), ERR_NULL),
     (dict(ws_bytes=8), ERR_WS),
@@ -64,7 +65,24 @@ def test_varlen_refuses(kw, code):
 
 
 @pytest.mark.parametrize("kw,code", SIZES + [
-    (dict(b=-1), ERR_SHAPE), (dict(state=None), ERR_NULL), (dict(q=None), ERR_NULL), (dict(y=fake(2)), ERR_ALIAS),
+    (dict(L=-1), ERR_SHAPE), (dict(b=65536), ERR_SHAPE), (dict(v=None), ERR_NULL), (dict(dy=None), ERR_NULL),
+    (dict(dk=None), ERR_NULL), (dict(dinit=None), ERR_NULL), (dict(ws=None), ERR_NULL), (dict(ws_bytes=300), ERR_WS),
+    (dict(dk=fake(4)), ERR_ALIAS), (dict(dq=fake(11)), ERR_ALIAS), (dict(dinit=fake(14)), ERR_ALIAS),
+    (dict(dfinal=fake(13)), ERR_ALIAS), (dict(dv=P(0x10000008)), ERR_SHAPE), (dict(b=0), OK),
+])
+def test_backward_refuses(kw, code):
+    a = dict(v=fake(1), g=fake(2), beta=fake(3), k=fake(4), q=fake(5), init=None, dy=fake(6), dfinal=None, dv=fake(8),
+             dg=fake(9), dbeta=fake(10), dk=fake(11), dq=fake(12), dinit=fake(13), b=2, L=100, H=4, P=16, N=16, G=1,
+             dtype=0, ws=fake(14), ws_bytes=1 << 30)
+    a.update(kw)
+    assert ssd.load_library().ssd_delta_backward(
+        a["v"], a["g"], a["beta"], a["k"], a["q"], a["init"], a["dy"], a["dfinal"], a["dv"], a["dg"], a["dbeta"],
+        a["dk"], a["dq"], a["dinit"], a["b"], a["L"], a["H"], a["P"], a["N"], a["G"], a["dtype"], a["ws"],
+        a["ws_bytes"], None) == code
+
+
+@pytest.mark.parametrize("kw,code", SIZES + [
+    (dict(b=-1), ERR_SHAPE), (dict(b=65535, H=257), ERR_SHAPE), (dict(state=None), ERR_NULL), (dict(q=None), ERR_NULL), (dict(y=fake(2)), ERR_ALIAS),
     (dict(y=fake(1)), ERR_ALIAS), (dict(state=P(0x10000004)), ERR_SHAPE), (dict(b=0), OK),
 ])
 def test_step_refuses(kw, code):

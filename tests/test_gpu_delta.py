@@ -244,6 +244,135 @@ def test_prefill_then_decode():
     check(torch.cat(ys, 1), S, ref.forward(d["v"], d["g"], d["beta"], d["k"], d["q"]), "bf16", 128)
 
 
+# ---- gradients --------------------------------------------------------------------------------------
+
+# (batch, seqlen, nheads, headdim, dstate, ngroups, dtype, init, kind)
+GRADS = [
+    (1, 1, 1, 16, 16, 1, "f32", False, "layer"),
+    (2, 1, 2, 64, 128, 1, "bf16", True, "layer"),
+    (2, 2, 3, 32, 16, 3, "bf16", False, "layer"),
+    (2, 33, 4, 16, 48, 2, "f32", True, "layer"),
+    (1, 64, 6, 64, 128, 1, "bf16", False, "layer"),
+    (2, 65, 2, 128, 64, 1, "bf16", True, "layer"),
+    (1, 97, 5, 64, 80, 5, "f32", False, "layer"),
+    (2, 129, 4, 64, 128, 2, "bf16", True, "layer"),
+    (1, 200, 3, 128, 256, 1, "bf16", True, "layer"),
+    (1, 130, 2, 128, 256, 2, "f32", True, "layer"),
+    (3, 260, 8, 32, 240, 1, "bf16", False, "layer"),
+    (1, 128, 20, 16, 32, 1, "f32", True, "layer"),
+    (2, 140, 4, 64, 128, 1, "bf16", True, "strong"),
+    (2, 140, 4, 32, 64, 2, "f32", True, "resets"),
+    (2, 140, 6, 64, 128, 2, "bf16", True, "resets"),
+    (1, 70, 2, 32, 64, 1, "f32", True, "repeat"),
+    (1, 700, 4, 64, 128, 1, "bf16", True, "layer"),
+]
+
+
+def grads(d):
+    import mamba_ssd_sequence_chunked_amd as ssd
+    return ssd.delta_backward(*inputs(d), dev(d["dy"], d["dtype"]), dev(d["init"]), dev(d["dfinal"]))
+
+
+def rel2(a, b):
+    return np.linalg.norm(a - b) / max(np.linalg.norm(b), 1e-300) if a.size else 0.0
+
+
+@pytest.mark.parametrize("c", GRADS, ids=ident)
+def test_backward(c):
+    """In the 2-norm: fp32 gradients to four of the state's units, the others to their three operands' and their own
+    rounding."""
+    import torch
+    b, L, H, P, N, G, dt, init, kind = c
+    d = ref.make(b, L, H, P, N, G, dt, init, seed=700 + GRADS.index(c), kind=kind)
+    got = grads(d)
+    torch.cuda.synchronize()
+    want = ref.backward(d["v"], d["g"], d["beta"], d["k"], d["q"], d["dy"], d["init"], d["dfinal"])
+    for n, w in want.items():
+        a = f64(got[n])
+        assert a.shape == w.shape and np.isfinite(a).all(), n
+        tol = 4 * state_unit(dt, N) + (4 * ROUND["bf16"] if dt == "bf16" and n in ("dv", "dk", "dq") else 0.0)
+        e = rel2(a, w)
+        print(f"{n} {e:.2e}", flush=True)
+        assert (a == 0).all() if not w.any() else e <= tol, (n, e, tol)
+
+
+def test_backward_keeps_fp32_accuracy_for_bf16_inputs():
+    d = ref.make(2, 600, 4, 64, 128, 2, "bf16", True, seed=31)
+    got = grads(d)
+    want = ref.backward(d["v"], d["g"], d["beta"], d["k"], d["q"], d["dy"], d["init"], d["dfinal"])
+    for n in ("dg", "dbeta", "dinit"):
+        assert rel2(f64(got[n]), want[n]) <= 1e-5, n
+
+
+def test_backward_against_differences():
+    """The gradients of the GPU's forward, by the GPU's backward: a step along a random direction."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(2, 45, 4, 16, 32, 2, "f32", True, seed=32)
+    got = {n: f64(t) for n, t in grads(d).items()}
+
+    def loss(x):
+        y, S = ssd.delta_forward(*inputs(x), dev(x["init"]))
+        return (f64(y) * d["dy"]).sum() + (f64(S) * d["dfinal"]).sum()
+
+    r = np.random.default_rng(1)
+    for n in ("v", "g", "beta", "k", "q", "init"):
+        step = 1e-2 * r.standard_normal(d[n].shape)
+        up, dn = dict(d), dict(d)
+        up[n], dn[n] = d[n] + step, d[n] - step
+        slope = (got["d" + n] * step).sum()
+        # the third-order term is about step^2 of the slope's terms; fp32 losses of about 30 differ by 1e-5
+        assert abs((loss(up) - loss(dn)) / 2 - slope) <= 2e-3 * np.linalg.norm(got["d" + n]) * np.linalg.norm(step) + 1e-4, n
+
+
+def test_backward_empty():
+    import torch
+    d = ref.make(2, 0, 4, 32, 64, 2, "bf16", True, seed=33)
+    got = grads(d)
+    assert torch.equal(got["dinit"], dev(d["dfinal"])) and got["dk"].shape == (2, 0, 2, 64)
+    assert grads(ref.make(0, 9, 4, 32, 64, 2, "f32", seed=33))["dinit"].numel() == 0
+
+
+def test_backward_repeats_bit_for_bit():
+    import torch
+    d = ref.make(2, 150, 8, 64, 128, 1, "bf16", True, seed=34)
+    a, b = grads(d), grads(d)
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+def test_training_step_captured_and_replayed():
+    """Forward and backward of one step in a graph, replayed on new inputs with eager work between."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    shape = (2, 130, 4, 64, 64, 1, "bf16", True)
+
+    def hand(seed):
+        d = ref.make(*shape, seed=seed)
+        return inputs(d) + [dev(d["dy"], "bf16"), dev(d["init"]), dev(d["dfinal"])]
+
+    x = hand(40)
+
+    def run():
+        return list(ssd.delta_forward(*x[:5], x[6])) + list(ssd.delta_backward(*x).values())
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = run()
+    for k in range(3):
+        for t, n in zip(x, hand(41 + k)):
+            t.copy_(n)
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        print(f"replay {k}", flush=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, w in zip(out, want):
+            assert torch.equal(a, w), k
+
+
 # ---- streams and graphs -----------------------------------------------------------------------------
 
 def test_on_another_stream():
