@@ -21,6 +21,8 @@
 // tokens at once, dq and dk, summed over the heads that share them inside a workgroup, in a fixed order.
 // Everything that leads to H, dbeta and dg is computed on pairs (fp32's accuracy for bf16 inputs); dq and dk,
 // which are rounded to T themselves, on T.
+#include <type_traits>
+
 #include "delta_tiles.hpp"
 
 namespace ssd {
@@ -46,20 +48,31 @@ struct RevCfg {
     static constexpr int kCH = NB * 32 * (int)sizeof(T) / 16, kCV = 16 * NW * (int)sizeof(T) / 16;
     static constexpr int kK = 0, kQ = DTile<kCH>::kBytes, kY = 2 * DTile<kCH>::kBytes, kR = kY + DTile<kCV>::kBytes;
     static constexpr int kStage = kR + R::kRevBytes;
+    static constexpr int kBuf = 2;
 };
 
+// 4 elements as they lie in memory, and as fp32
+__device__ __forceinline__ u32x2 load_raw(const bf16* p) { return *reinterpret_cast<const u32x2*>(p); }
+__device__ __forceinline__ u32x4 load_raw(const float* p) { return *reinterpret_cast<const u32x4*>(p); }
+__device__ __forceinline__ f32x4 raw_f32(u32x2 v)
+{
+    const bf16x4 q = __builtin_bit_cast(bf16x4, v);
+    return f32x4{(float)q[0], (float)q[1], (float)q[2], (float)q[3]};
+}
+__device__ __forceinline__ f32x4 raw_f32(u32x4 v) { return __builtin_bit_cast(f32x4, v); }
+
 template <typename T, int NB, int NW>
-__global__ __launch_bounds__(64 * NW) void delta_rev_kernel(
+__device__ __forceinline__ void walk_back(
     const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ dfinal,
     const unsigned char* __restrict__ recs, T* __restrict__ dv, float* __restrict__ dinit, DeltaKeep<T> keep,
     DeltaBack<T> back, DeltaDims d, int nslice)
 {
     using C = RevCfg<T, NB, NW>;
     using R = DeltaRec<T, true>;
-    constexpr int kBuf = 2;
+    constexpr int kBuf = C::kBuf;
     static_assert(kBuf * C::kStage <= 160 * 1024, "ring");
-    __shared__ __attribute__((aligned(1024))) unsigned char ring[kBuf * C::kStage];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char ring[];        // kBuf * C::kStage
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int bid = xcd_logical_block(blockIdx.x, gridDim.x);
     const int slice = bid % nslice;
     const int64_t sh = bid / nslice, s = sh / d.nheads;
@@ -77,87 +90,153 @@ __global__ __launch_bounds__(64 * NW) void delta_rev_kernel(
     const T* ybase = keep.dy + (sq.start * d.nheads + h) * P + pw;
     const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)R::kBytes + R::kM;
     const unsigned lds0 = lds_addr(&ring[0]);
+    const WRows<T, C::kCH> krows(r, g);
+    const WCols<T, C::kCH> kcols(r, g);
+    const WCols<T, kRecCH<T>> rcols(r, g);
+    DTileCopy<C::kCH, NW, WTile<C::kCH>> kcopy;
+    DTileCopy<C::kCV, NW, VTile<C::kCV>> vcopy;
+    kcopy.plan(krow, wave, lane);
+    vcopy.plan(vrow, wave, lane);
 
     if (valid < C::kCH) {
         for (int i = threadIdx.x; i < kBuf * 32 * C::kCH; i += 64 * NW) {
             const int row = (i / C::kCH) % 32, b = i / (32 * C::kCH), c = i % C::kCH;
             if (c >= valid) {
-                unsigned char* st = ring + b * C::kStage + DTile<C::kCH>::offset(row, c);
+                unsigned char* st = ring + b * C::kStage + WTile<C::kCH>::offset(row, c);
                 *reinterpret_cast<uint4*>(st + C::kK) = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4*>(st + C::kQ) = make_uint4(0, 0, 0, 0);
             }
         }
         __syncthreads();
     }
-    auto issue = [&](int c) {
-        const unsigned st = lds0 + (unsigned)(c % kBuf) * C::kStage;
-        const int rmax = min(kDC, sq.len - c * kDC) - 1;
-        const int64_t tok = (int64_t)c * kDC;
-        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(kbase) + tok * krow, krow, rmax, valid,
-                               st + C::kK, wave, lane);
-        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(qbase) + tok * krow, krow, rmax, valid,
-                               st + C::kQ, wave, lane);
-        dtile_copy<C::kCV, NW>(reinterpret_cast<const unsigned char*>(ybase) + tok * vrow, vrow, rmax, C::kCV,
-                               st + C::kY, wave, lane);
-        linear_copy<R::kRevBytes, NW>(rbase + (int64_t)c * d.nheads * R::kBytes, st + C::kR, wave, lane);
+    // the copies of block c (called from the last to the first) into stage b
+    const int last = nblk > 0 ? nblk - 1 : 0;
+    const unsigned char* kp = reinterpret_cast<const unsigned char*>(kbase) + (uint64_t)krow * kDC * last;
+    const unsigned char* qp = reinterpret_cast<const unsigned char*>(qbase) + (uint64_t)krow * kDC * last;
+    const unsigned char* yp = reinterpret_cast<const unsigned char*>(ybase) + (uint64_t)vrow * kDC * last;
+    const unsigned char* rp = rbase + (int64_t)last * d.nheads * R::kBytes;
+    auto issue = [&](int c, int b) __attribute__((always_inline)) {
+        const unsigned st = lds0 + (unsigned)b * C::kStage;
+        const int rows = sq.len - c * kDC;
+        kcopy.issue(kp, krow, rows, valid, st + C::kK, wave, lane);
+        kcopy.issue(qp, krow, rows, valid, st + C::kQ, wave, lane);
+        vcopy.issue(yp, vrow, rows, C::kCV, st + C::kY, wave, lane);
+        linear_copy<R::kRevBytes, NW>(rp, st + C::kR, wave, lane);
+        kp -= (uint64_t)krow * kDC;
+        qp -= (uint64_t)krow * kDC;
+        yp -= (uint64_t)vrow * kDC;
+        rp -= d.nheads * R::kBytes;
     };
 
+    auto ncol = [&](int t) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); };        // as in the walk forward
     f32x4 H[2 * NB];
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t) {
         H[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (dfinal && 16 * t < N) {
-            const float4 a = *reinterpret_cast<const float4*>(dfinal + (sh * P + p) * N + 16 * t + 4 * g);
+        if (dfinal && ncol(t) < N) {
+            const float4 a = *reinterpret_cast<const float4*>(dfinal + (sh * P + p) * N + ncol(t));
             H[t] = f32x4{a.x, a.y, a.z, a.w};
         }
     }
-    // <H, S> over this wavefront's rows at the start of chunk k (or the end)
-    auto put_inner = [&](int k) {
-        const int64_t as = ((s * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
+    // S at the start of chunk k (or the end), as it is kept, for <H, S> over this wavefront's rows. Where registers
+    // allow, it is fetched a block ahead.
+    constexpr bool kAhead = NB * sizeof(T) <= 8;
+    typedef decltype(load_raw(static_cast<const T*>(nullptr))) Raw;
+    Raw shi[kAhead ? 2 * NB : 1], slo[kAhead && sizeof(T) == 2 ? 2 * NB : 1];
+    auto at_S = [&](int k) { return ((s * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N; };
+    auto fetch_S = [&](int k) __attribute__((always_inline)) {
+        if constexpr (kAhead) {
+            const int64_t at = at_S(k);
+#pragma unroll
+            for (int t = 0; t < 2 * NB; ++t) {
+                if (ncol(t) < N) {
+                    shi[t] = load_raw(keep.S + at + ncol(t));
+                    if constexpr (sizeof(T) == 2) slo[t] = load_raw(keep.Slo + at + ncol(t));
+                }
+            }
+        }
+    };
+    auto put_inner = [&](int k) __attribute__((always_inline)) {
+        const int64_t at = at_S(k);
         float dot = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
-            if (16 * t < N) {
-                const float4 a = load4f(keep.S + as + 16 * t + 4 * g);
-                dot += H[t][0] * a.x + H[t][1] * a.y + H[t][2] * a.z + H[t][3] * a.w;
-                if (sizeof(T) == 2) {
-                    const float4 l = load4f(keep.Slo + as + 16 * t + 4 * g);
-                    dot += H[t][0] * l.x + H[t][1] * l.y + H[t][2] * l.z + H[t][3] * l.w;
+            if (ncol(t) < N) {
+                const f32x4 a = raw_f32(kAhead ? shi[kAhead ? t : 0] : load_raw(keep.S + at + ncol(t)));
+                dot += H[t][0] * a[0] + H[t][1] * a[1] + H[t][2] * a[2] + H[t][3] * a[3];
+                if constexpr (sizeof(T) == 2) {
+                    const f32x4 l = raw_f32(kAhead ? slo[kAhead ? t : 0] : load_raw(keep.Slo + at + ncol(t)));
+                    dot += H[t][0] * l[0] + H[t][1] * l[1] + H[t][2] * l[2] + H[t][3] * l[3];
                 }
             }
         }
         dot = group_sum<64>(dot);
         if (lane == 0) back.hs[((pt * d.seqs + s) * (keep.chunks + 1) + k) * d.nheads + h] = dot;
     };
-    wait_vmem();
-    if (nblk > 0) issue(nblk - 1);
-
-    for (int c = nblk - 1; c >= 0; --c) {
-        wait_vmem();
-        __syncthreads();
-        // this block's rows of v and its e, in the form lane = token, 4 columns
-        float4 vv[2], ev[2];
+    // v and e of this lane's tokens and 4 columns in the columns = tokens form, fetched a block ahead
+    Raw vv[2], vn[2];
+    f32x4 ev[2], en[2];
+    auto fetch_ve = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            const int64_t tok = sq.start + min(c * kDC + 16 * t + r, sq.len - 1);
-            vv[t] = load4f(v + (tok * d.nheads + h) * P + 16 * pt + 4 * g);
-            ev[t] = load4f(keep.e + keep.frag(sq.slot + c, h, pt, d) + t * 256 + lane * 4);
+            const int64_t tok = sq.start + min(c * kDC + perm32(t, r), sq.len - 1);
+            vn[t] = load_raw(v + (tok * d.nheads + h) * P + 16 * pt + 4 * g);
+            en[t] = *reinterpret_cast<const f32x4*>(keep.e + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g));
         }
+    };
+    if (nblk > 0) {
+        fetch_S((nblk + 1) / 2);
+        fetch_ve(nblk - 1);
+    } else {
+        fetch_S(0);
+    }
+    wait_vmem();
+    if (nblk > 0) issue(nblk - 1, 0);
+
+    auto step = [&](int c, auto stage) __attribute__((always_inline)) {
+        constexpr int b = decltype(stage)::value;
+        // (see the walk forward; the loads ahead of the next block were started before its copies)
+        constexpr int kStores = 8;
+        if (c < nblk - 1) wait_vmem_below<kStores>(); else wait_vmem();
+        __syncthreads();
         if (c % 2 == 1 || c == nblk - 1) {
             const int k = c / 2;
             const int64_t at = ((s * keep.chunks + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
 #pragma unroll
             for (int t = 0; t < 2 * NB; ++t)
-                if (16 * t < N) store4(back.H + at + 16 * t + 4 * g, H[t][0], H[t][1], H[t][2], H[t][3]);
+                if (ncol(t) < N) store4(back.H + at + ncol(t), H[t][0], H[t][1], H[t][2], H[t][3]);
             put_inner(k + 1);
         }
-        if (c > 0) issue(c - 1);
-        const unsigned char* st = ring + (c % kBuf) * C::kStage;
-        const unsigned char* rec = st + C::kR - R::kM;
-        const float* tab = reinterpret_cast<const float*>(rec + R::kTab);
+        if (c % 2 == 0) fetch_S(c / 2);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            vv[t] = vn[t];
+            ev[t] = en[t];
+        }
+        if (c > 0) {
+            fetch_ve(c - 1);
+            issue(c - 1, 1 - b);
+        }
+        const unsigned st = lds0 + b * C::kStage, rec = st + C::kR - R::kM, tab = rec + R::kTab;
         const int rows = min(kDC, sq.len - c * kDC);
 
-        // dU = M^T dY + del K H^T (rows tokens, columns p)
+        // what does not depend on H first
+        Vec8<T> yf;
+        Pair<T> mt[2], bm[2];
+        float ga[8], de[8], bt8[8], bet[2];
+        vtile_cols<C::kCV>(yf, st + C::kY, wave, r, g);
+        tab_rows(ga, tab, g);
+        tab_rows(de, tab + 128, g);
+        tab_rows(bt8, tab + 256, g);
+        const float gl = lds_at<float>(tab + 124);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            load_pair(mt[t], rcols, rec + R::kM, t);
+            load_pair(bm[t], rcols, rec + R::kB, t);
+            bet[t] = lds_at<float>(tab + 256 + 4 * perm32(t, r));
+        }
+
+        // dU = M^T dY + del K H^T (rows tokens, columns p; rows past the sequence are zero, as their dY and K are)
         f32x4 kh[2], du[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) kh[t] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -170,88 +249,94 @@ __global__ __launch_bounds__(64 * NW) void delta_rev_kernel(
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 Vec8<T> kf;
-                dtile_row<C::kCH>(kf, st + C::kK, 16 * t + r, kb, g);
+                krows.load(kf, st + C::kK, t, kb);
                 mma_xp(kh[t], kf, hp);
             }
-        }
-        Vec8<T> yf;
-        dtile_col<C::kCV>(yf, st + C::kY, 16 * wave, r, g);
-        if (rows < kDC) {
-            // the copies repeat the last row: rows past the sequence carry no gradient
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if ((i & 3) + 4 * g + (i >> 2) * 16 >= rows) yf.set(i, 0.f);
         }
         float dU[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int row = 16 * t + 4 * g + m;
-                du[t][m] = row < rows ? kh[t][m] * tab[32 + row] : 0.f;
-            }
-            Pair<T> mt;
-            rec_cols(mt, rec + R::kM, t, r, g);
-            mma_px(du[t], mt, yf);
+            for (int m = 0; m < 4; ++m) du[t][m] = kh[t][m] * de[4 * t + m];
+            mma_px(du[t], mt[t], yf);
 #pragma unroll
             for (int m = 0; m < 4; ++m) dU[4 * t + m] = du[t][m];
         }
         Pair<T> dup;
         dup.set(dU);
-        // w = B^T dU in both forms: rows tokens (to go on with) and columns tokens (to hand out)
+        // w = B^T dU in both forms: rows tokens (to go on with) and columns tokens (to hand out). Rows past the
+        // sequence are outside the buffers: dropped.
+        const int64_t th = (sq.start + c * kDC) * d.nheads + h;
+        const auto odv = __builtin_amdgcn_make_buffer_rsrc(dv + th * P + 16 * pt, 0, (rows - 1) * (int)vrow + 16 * (int)sizeof(T), kBufferDword3);
+        const auto ovd = __builtin_amdgcn_make_buffer_rsrc(back.vdv + pt * d.tokens * d.nheads + th, 0, (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
+        const auto owe = __builtin_amdgcn_make_buffer_rsrc(back.we + pt * d.tokens * d.nheads + th, 0, (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
         float bw[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            Pair<T> bt;
-            rec_cols(bt, rec + R::kB, t, r, g);
-            f32x4 w = {0.f, 0.f, 0.f, 0.f}, wt = w;
-            mma_pp(w, bt, dup);
-            mma_pp(wt, dup, bt);
+            Vec8<T> one;
+            unit_frag(one, t, r, g);
+            f32x4 w = du[t], wt = {0.f, 0.f, 0.f, 0.f};
+            mma_pp(w, bm[t], dup);
+            mma_pp(wt, dup, bm[t]);
+            mma_px(wt, dup, one);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int row = 16 * t + 4 * g + m;
-                bw[4 * t + m] = -tab[row] * tab[64 + row] * w[m];
-            }
-            store4(back.w + keep.frag(sq.slot + c, h, pt, d) + t * 256 + lane * 4, wt[0], wt[1], wt[2], wt[3]);
-            float we = wt[0] * ev[t].x + wt[1] * ev[t].y + wt[2] * ev[t].z + wt[3] * ev[t].w;
-            const float be = tab[64 + 16 * t + r];
-            wt *= be;
-            float vd = wt[0] * vv[t].x + wt[1] * vv[t].y + wt[2] * vv[t].z + wt[3] * vv[t].w;
+            for (int m = 0; m < 4; ++m) bw[4 * t + m] = -ga[4 * t + m] * bt8[4 * t + m] * w[m];
+            store4(back.w + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g), wt[0], wt[1], wt[2], wt[3]);
+            float we = wt[0] * ev[t][0] + wt[1] * ev[t][1] + wt[2] * ev[t][2] + wt[3] * ev[t][3];
+            wt *= bet[t];
+            const f32x4 vf = raw_f32(vv[t]);
+            float vd = wt[0] * vf[0] + wt[1] * vf[1] + wt[2] * vf[2] + wt[3] * vf[3];
             we += __shfl_xor(we, 16, kWave);
             vd += __shfl_xor(vd, 16, kWave);
             we += __shfl_xor(we, 32, kWave);
             vd += __shfl_xor(vd, 32, kWave);
-            if (16 * t + r < rows) {
-                const int64_t th = (sq.start + c * kDC + 16 * t + r) * d.nheads + h;
-                store4(dv + th * P + 16 * pt + 4 * g, wt[0], wt[1], wt[2], wt[3]);
-                if (g == 0) {
-                    back.vdv[pt * d.tokens * d.nheads + th] = vd;
-                    back.we[pt * d.tokens * d.nheads + th] = we;
-                }
-            }
+            const int tok = perm32(t, r);
+            buffer_store4(odv, tok * (int)vrow + 4 * g * (int)sizeof(T), 0, wt, T());
+            // (the four lane groups hold the same sums)
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(vd), ovd, tok * (int)d.nheads * 4, 0, 0);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(we), owe, tok * (int)d.nheads * 4, 0, 0);
         }
         // H before the block = gam_last H + Q^T (gam dY) - K^T (beta gam w)
         float gy[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) gy[i] = tab[(i & 3) + 4 * g + (i >> 2) * 16] * yf.get(i);
+        for (int i = 0; i < 8; ++i) gy[i] = ga[i] * yf.get(i);
         Pair<T> gyp, bwp;
         gyp.set(gy);
         bwp.set(bw);
-        const float gl = tab[31];
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             H[t] *= gl;
             Vec8<T> qf, kf;
-            dtile_col<C::kCH>(qf, st + C::kQ, 16 * t, r, g);
+            kcols.load(qf, st + C::kQ, t & 1, t >> 1);
             mma_xp(H[t], qf, gyp);
-            dtile_col<C::kCH>(kf, st + C::kK, 16 * t, r, g);
+            kcols.load(kf, st + C::kK, t & 1, t >> 1);
             mma_xp(H[t], kf, bwp);
         }
+    };
+    for (int c = nblk - 1; c >= 0; c -= 2) {
+        step(c, std::integral_constant<int, 0>());
+        if (c > 0) step(c - 1, std::integral_constant<int, 1>());
     }
     put_inner(0);
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t)
-        if (16 * t < N) store4(dinit + (sh * P + p) * N + 16 * t + 4 * g, H[t][0], H[t][1], H[t][2], H[t][3]);
+        if (ncol(t) < N) store4(dinit + (sh * P + p) * N + ncol(t), H[t][0], H[t][1], H[t][2], H[t][3]);
+}
+
+// (registers: see delta_chain_kernel)
+template <typename T, int NB, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_rev_kernel(
+    const T* v, const T* Km, const T* Qm, const float* dfinal, const unsigned char* recs, T* dv, float* dinit,
+    DeltaKeep<T> keep, DeltaBack<T> back, DeltaDims d, int nslice)
+{
+    walk_back<T, NB, NW>(v, Km, Qm, dfinal, recs, dv, dinit, keep, back, d, nslice);
+}
+template <typename T, int NB, int NW>
+__global__ __launch_bounds__(64 * NW) void delta_rev_f32_kernel(
+    const T* v, const T* Km, const T* Qm, const float* dfinal, const unsigned char* recs, T* dv, float* dinit,
+    DeltaKeep<T> keep, DeltaBack<T> back, DeltaDims d, int nslice)
+{
+    walk_back<T, NB, NW>(v, Km, Qm, dfinal, recs, dv, dinit, keep, back, d, nslice);
 }
 
 // ---- dbeta and dg ---------------------------------------------------------------------------------------------
@@ -263,7 +348,7 @@ __global__ __launch_bounds__(256) void delta_scalar_kernel(
     int nseg, int hblocks, int zero_first)
 {
     __shared__ double part[4][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
     const int hb = blockIdx.x % hblocks;
     const int seg = (blockIdx.x / hblocks) % nseg;
     const int64_t s = blockIdx.x / hblocks / nseg;
@@ -333,7 +418,7 @@ struct KqCfg {
 // A workgroup = one 64-token chunk of one (row, group) and a range of the group's heads; a wavefront = 16 of the
 // tokens and all N columns of dq and dk (as rows n, columns = tokens).
 template <typename T, int NB>
-__global__ __launch_bounds__(256) void delta_kq_kernel(
+__global__ __launch_bounds__(256, 2) void delta_kq_kernel(
     const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ gv, const float* __restrict__ bv,
     DeltaKeep<T> keep, DeltaBack<T> back, T* __restrict__ dq, T* __restrict__ dk, float* __restrict__ partial,
     DeltaDims d, int nslice)
@@ -343,7 +428,7 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
     __shared__ __attribute__((aligned(16))) unsigned char ub[2][C::kU];
     __shared__ double cst[4][64];
     __shared__ float bet[4][64];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int slice = blockIdx.x % nslice;
     const int grp = (blockIdx.x / nslice) % d.ngroups;
     const int64_t sk = blockIdx.x / nslice / d.ngroups, s = sk / keep.chunks;
@@ -361,6 +446,9 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
     const int mine = 16 * wave + r;                           // this lane's token in operand fragments
     const bool tok = mine < rows;
     const unsigned lds0 = lds_addr(&ring[0]);
+    const DCols<T, C::kCH> cols(r, g);
+    DTileCopy<C::kCH, 4> scopy;
+    scopy.plan((unsigned)(N * sizeof(T)), wave, lane);
 
     auto zero_pad = [&](int tiles) {
         for (int i = threadIdx.x; i < tiles * 32 * C::kCH; i += 256) {
@@ -374,19 +462,19 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
         zero_pad(4);
         __syncthreads();
     }
-    auto issue = [&](int i) {
+    auto issue = [&](int i) __attribute__((always_inline)) {
         const int h = h0 + i / nkb, kb = i % nkb;
         const unsigned st = lds0 + (unsigned)(i & 1) * C::kStage;
-        const int rmax = min(32, P - 32 * kb) - 1;
+        const int rows = P - 32 * kb;
         const int64_t pn = (int64_t)P * N, off = (int64_t)32 * kb * N;
-        dtile_copy<C::kCH, 4>(keep.S + ((s * (keep.chunks + 1) + k) * d.nheads + h) * pn + off,
-                              (unsigned)(N * sizeof(T)), rmax, valid, st, wave, lane);
-        dtile_copy<C::kCH, 4>(back.H + ((s * keep.chunks + k) * d.nheads + h) * pn + off, (unsigned)(N * sizeof(T)),
-                              rmax, valid, st + C::kTile, wave, lane);
+        scopy.issue(keep.S + ((s * (keep.chunks + 1) + k) * d.nheads + h) * pn + off, (unsigned)(N * sizeof(T)), rows,
+                    valid, st, wave, lane);
+        scopy.issue(back.H + ((s * keep.chunks + k) * d.nheads + h) * pn + off, (unsigned)(N * sizeof(T)), rows, valid,
+                    st + C::kTile, wave, lane);
     };
     // the operands of a stage in registers: lane = token, slots = columns {4g .., 16 + 4g ..} of 32
     struct Ops { float4 y[2], e[2], w[2]; float gr, be; };
-    auto fetch = [&](int i) {
+    auto fetch = [&](int i) __attribute__((always_inline)) {
         Ops o;
         const int h = h0 + i / nkb, kb = i % nkb;
 #pragma unroll
@@ -454,12 +542,12 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
             issue(i + 1);
             cur = fetch(i + 1);
         }
-        const unsigned char* st = ring + (i & 1) * C::kStage;
+        const unsigned st = lds0 + (unsigned)(i & 1) * C::kStage;
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             Vec8<T> sf, hf;
-            dtile_col<C::kCH>(sf, st, 16 * t, r, g);
-            dtile_col<C::kCH>(hf, st + C::kTile, 16 * t, r, g);
+            cols.load(sf, st, t);
+            cols.load(hf, st + C::kTile, t);
             mma(aq[t], sf, gy);
             mma(ak[t], hf, du);
             mma(ak[t], sf, bw);
@@ -507,27 +595,29 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
             *reinterpret_cast<T*>(zl + o) = from_f32<T>(Zs[t][m]);
         }
     }
-    auto load_rows = [&](const T* m) {
+    DTileCopy<C::kCH, 4> kcopy;
+    kcopy.plan((unsigned)(d.ngroups * N * sizeof(T)), wave, lane);
+    auto load_rows = [&](const T* m) __attribute__((always_inline)) {
         for (int b = 0; b < 2; ++b) {
-            // a second half past the sequence reads the first half's last row (its weights are zero)
-            const int first = min(32 * b, rows - 1), rmax = min(32, rows - first) - 1;
-            dtile_copy<C::kCH, 4>(m + ((t0 + first) * d.ngroups + grp) * N, (unsigned)(d.ngroups * N * sizeof(T)), rmax,
-                                  valid, lds0 + b * C::kTile, wave, lane);
+            kcopy.issue(m + ((t0 + 32 * b) * d.ngroups + grp) * N, (unsigned)(d.ngroups * N * sizeof(T)), rows - 32 * b,
+                        valid, lds0 + b * C::kTile, wave, lane);
         }
         wait_vmem();
         __syncthreads();
     };
+    const unsigned wl0 = lds0 + 2 * C::kTile;
+    const DRows<T, C::kCW> wrows(r, g);
     load_rows(Km);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         Vec8<T> wr, zr, zc;
-        dtile_row<C::kCW>(wr, wl + (wave >> 1) * DTile<C::kCW>::kBytes, 16 * (wave & 1) + r, b, g);
-        dtile_row<C::kCW>(zr, zl + (wave >> 1) * DTile<C::kCW>::kBytes, 16 * (wave & 1) + r, b, g);
-        dtile_col<C::kCW>(zc, zl + b * DTile<C::kCW>::kBytes, 16 * wave, r, g);
+        wrows.load(wr, wl0 + (wave >> 1) * DTile<C::kCW>::kBytes, wave & 1, b);
+        wrows.load(zr, wl0 + C::kWz + (wave >> 1) * DTile<C::kCW>::kBytes, wave & 1, b);
+        DCols<T, C::kCW>::load_any(zc, wl0 + C::kWz + b * DTile<C::kCW>::kBytes, wave, r, g);
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             Vec8<T> kf;
-            dtile_col<C::kCH>(kf, ring + b * C::kTile, 16 * t, r, g);
+            cols.load(kf, lds0 + b * C::kTile, t);
             mma(aq[t], kf, wr);
             mma(ak[t], kf, zr);
             mma(ak[t], kf, zc);
@@ -538,11 +628,11 @@ __global__ __launch_bounds__(256) void delta_kq_kernel(
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
         Vec8<T> wc;
-        dtile_col<C::kCW>(wc, wl + b * DTile<C::kCW>::kBytes, 16 * wave, r, g);
+        DCols<T, C::kCW>::load_any(wc, wl0 + b * DTile<C::kCW>::kBytes, wave, r, g);
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             Vec8<T> qf;
-            dtile_col<C::kCH>(qf, ring + b * C::kTile, 16 * t, r, g);
+            cols.load(qf, lds0 + b * C::kTile, t);
             mma(ak[t], qf, wc);
         }
     }
@@ -622,8 +712,14 @@ hipError_t launch_rev(const T* v, const T* k, const T* q, const float* dfinal, c
                       hipStream_t stream)
 {
     const int nslice = (int)d.headdim / (16 * NW);
-    hipLaunchKernelGGL((delta_rev_kernel<T, NB, NW>), dim3((unsigned)(d.seqs * d.nheads * nslice)), dim3(64 * NW), 0,
-                       stream, v, k, q, dfinal, rec, dv, dinit, keep, back, d, nslice);
+    const dim3 grid((unsigned)(d.seqs * d.nheads * nslice));
+    constexpr unsigned kLds = RevCfg<T, NB, NW>::kBuf * RevCfg<T, NB, NW>::kStage;
+    if constexpr (sizeof(T) == 2)
+        hipLaunchKernelGGL((delta_rev_kernel<T, NB, NW>), grid, dim3(64 * NW), kLds, stream, v, k, q, dfinal, rec, dv,
+                           dinit, keep, back, d, nslice);
+    else
+        hipLaunchKernelGGL((delta_rev_f32_kernel<T, NB, NW>), grid, dim3(64 * NW), kLds, stream, v, k, q, dfinal, rec, dv,
+                           dinit, keep, back, d, nslice);
     return hipGetLastError();
 }
 

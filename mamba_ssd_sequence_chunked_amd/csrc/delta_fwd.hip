@@ -17,6 +17,8 @@
 //
 // A workgroup = NW wavefronts = 16 NW rows of one (sequence, head).  K, Q, the V columns and the block's record come
 // through a ring of NBUF stages of asynchronous global -> LDS copies; one barrier per block.
+#include <type_traits>
+
 #include "delta_tiles.hpp"
 
 namespace ssd {
@@ -38,7 +40,7 @@ struct ChainCfg {
 };
 
 template <typename T, int NB, int NW, bool kBwd>
-__global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
+__device__ __forceinline__ void chain(
     const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ init,
     const unsigned char* __restrict__ recs, T* __restrict__ y, float* __restrict__ fin, DeltaKeep<T> keep, DeltaDims d,
     int nslice)
@@ -47,8 +49,8 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     using R = DeltaRec<T, kBwd>;
     constexpr int kBuf = C::kBuf;
     static_assert(kBuf >= 2 && kBuf * C::kStage <= 160 * 1024, "ring");
-    __shared__ __attribute__((aligned(1024))) unsigned char ring[kBuf * C::kStage];
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
+    extern __shared__ __attribute__((aligned(1024))) unsigned char ring[];        // kBuf * C::kStage
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int bid = xcd_logical_block(blockIdx.x, gridDim.x);
     const int slice = bid % nslice;
     const int64_t sh = bid / nslice;
@@ -65,16 +67,22 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     const T* kbase = Km + (sq.start * d.ngroups + grp) * N;
     const T* qbase = Qm + (sq.start * d.ngroups + grp) * N;
     const T* vbase = v + (sq.start * d.nheads + h) * P + pw;
-    T* ybase = y + (sq.start * d.nheads + h) * P + pw + 16 * wave;
     const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)R::kBytes;
     const unsigned lds0 = lds_addr(&ring[0]);
+    const WRows<T, C::kCH> krows(r, g);
+    const WCols<T, C::kCH> kcols(r, g);
+    const WRows<T, kRecCH<T>> rrows(r, g);
+    DTileCopy<C::kCH, NW, WTile<C::kCH>> kcopy;
+    DTileCopy<C::kCV, NW, VTile<C::kCV>> vcopy;
+    kcopy.plan(krow, wave, lane);
+    vcopy.plan(vrow, wave, lane);
 
     if (valid < C::kCH) {
         // columns past N are never copied: zero them once, so that the state's rows there stay zero
         for (int i = threadIdx.x; i < kBuf * 32 * C::kCH; i += 64 * NW) {
             const int row = (i / C::kCH) % 32, b = i / (32 * C::kCH), c = i % C::kCH;
             if (c >= valid) {
-                unsigned char* st = ring + b * C::kStage + DTile<C::kCH>::offset(row, c);
+                unsigned char* st = ring + b * C::kStage + WTile<C::kCH>::offset(row, c);
                 *reinterpret_cast<uint4*>(st + C::kK) = make_uint4(0, 0, 0, 0);
                 *reinterpret_cast<uint4*>(st + C::kQ) = make_uint4(0, 0, 0, 0);
             }
@@ -82,69 +90,102 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
         __syncthreads();
     }
 
-    auto issue = [&](int c) {
-        const unsigned st = lds0 + (unsigned)(c % kBuf) * C::kStage;
-        const int rmax = min(kDC, sq.len - c * kDC) - 1;
-        const int64_t tok = (int64_t)c * kDC;
-        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(kbase) + tok * krow, krow, rmax, valid,
-                               st + C::kK, wave, lane);
-        dtile_copy<C::kCH, NW>(reinterpret_cast<const unsigned char*>(qbase) + tok * krow, krow, rmax, valid,
-                               st + C::kQ, wave, lane);
-        dtile_copy<C::kCV, NW>(reinterpret_cast<const unsigned char*>(vbase) + tok * vrow, vrow, rmax, C::kCV,
-                               st + C::kV, wave, lane);
-        linear_copy<R::kFwdBytes, NW>(rbase + (int64_t)c * d.nheads * R::kBytes, st + C::kR, wave, lane);
+    // the copies of block c (called in order) into stage b
+    const unsigned char* kp = reinterpret_cast<const unsigned char*>(kbase);
+    const unsigned char* qp = reinterpret_cast<const unsigned char*>(qbase);
+    const unsigned char* vp = reinterpret_cast<const unsigned char*>(vbase);
+    const unsigned char* rp = rbase;
+    auto issue = [&](int c, int b) __attribute__((always_inline)) {
+        const unsigned st = lds0 + (unsigned)b * C::kStage;
+        const int rows = sq.len - c * kDC;
+        kcopy.issue(kp, krow, rows, valid, st + C::kK, wave, lane);
+        kcopy.issue(qp, krow, rows, valid, st + C::kQ, wave, lane);
+        vcopy.issue(vp, vrow, rows, C::kCV, st + C::kV, wave, lane);
+        linear_copy<R::kFwdBytes, NW>(rp, st + C::kR, wave, lane);
+        kp += (uint64_t)krow * kDC;
+        qp += (uint64_t)krow * kDC;
+        vp += (uint64_t)vrow * kDC;
+        rp += d.nheads * R::kBytes;
     };
 
+    // S^T in accumulator tiles: tile t = 2 kb + x, rows 4g + m = columns ncol(t) + m of the state, column r = its row p
+    auto ncol = [&](int t) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); };
     f32x4 S[2 * NB];
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t) {
         S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (init && 16 * t < N) {
-            const float4 a = *reinterpret_cast<const float4*>(init + (sh * P + p) * N + 16 * t + 4 * g);
+        if (init && ncol(t) < N) {
+            const float4 a = *reinterpret_cast<const float4*>(init + (sh * P + p) * N + ncol(t));
             S[t] = f32x4{a.x, a.y, a.z, a.w};
         }
     }
     wait_vmem();          // so that no register load is in flight among the copies that are counted below
 #pragma unroll
     for (int c = 0; c < kBuf - 1; ++c)
-        if (c < nblk) issue(c);
+        if (c < nblk) issue(c, c);
 
     // the state entering a chunk of 64 tokens (k = 0 ..) and after the last one
-    auto keep_state = [&](int k) {
+    auto keep_state = [&](int k) __attribute__((always_inline)) {
         const int64_t at = (((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
-            if (16 * t < N) {
-                store4(keep.S + at + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
+            if (ncol(t) < N) {
+                store4(keep.S + at + ncol(t), S[t][0], S[t][1], S[t][2], S[t][3]);
                 if (sizeof(T) == 2) {
                     float lo[4];
 #pragma unroll
                     for (int m = 0; m < 4; ++m) lo[m] = S[t][m] - to_f32(from_f32<T>(S[t][m]));
-                    store4(keep.Slo + at + 16 * t + 4 * g, lo[0], lo[1], lo[2], lo[3]);
+                    store4(keep.Slo + at + ncol(t), lo[0], lo[1], lo[2], lo[3]);
                 }
             }
         }
     };
 
-    for (int c = 0; c < nblk; ++c) {
-        // this stage's copies are done when no more than the later stages' are outstanding
-        constexpr int kLater = (kBuf - 2) * C::kMin < 63 ? (kBuf - 2) * C::kMin : 63;
-        if (c + kBuf - 2 < nblk) wait_vmem_below<kLater>(); else wait_vmem();
+    // dy of this lane's tokens and 4 columns in the columns = tokens form, fetched a block ahead
+    f32x4 dyv[2], dyn[2];
+    auto fetch_dy = [&](f32x4 (&o)[2], int c) __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            const int64_t tok = sq.start + min(c * kDC + perm32(t, r), sq.len - 1);
+            const float4 f = load4f(keep.dy + (tok * d.nheads + h) * P + pw + 16 * wave + 4 * g);
+            o[t] = f32x4{f.x, f.y, f.z, f.w};
+        }
+    };
+    // block c in stage b (a constant: the loop is unrolled over the ring)
+    auto step = [&](int c, auto stage) __attribute__((always_inline)) {
+        constexpr int b = decltype(stage)::value;
+        // This stage's copies are done when what was started after them is all that is outstanding (the counter goes
+        // down in order): the later stages' copies and the last block's kStores stores.
+        constexpr int kStores = kBwd ? 4 : 2;
+        constexpr int kLater = (kBuf - 2) * C::kMin < 63 - kStores ? (kBuf - 2) * C::kMin : 63 - kStores;
+        if (c + kBuf - 2 >= nblk) wait_vmem();
+        else if (c > 0) wait_vmem_below<kLater + kStores>();
+        else wait_vmem_below<kLater>();
         __syncthreads();                                  // and everybody is done with the stage before it
-        float4 dyv[2];
         if constexpr (kBwd) {
             if (c % 2 == 0) keep_state(c / 2);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int64_t tok = sq.start + min(c * kDC + 16 * t + r, sq.len - 1);
-                dyv[t] = load4f(keep.dy + (tok * d.nheads + h) * P + pw + 16 * wave + 4 * g);
-            }
+            for (int t = 0; t < 2; ++t) dyv[t] = dyn[t];
+            if (c + 1 < nblk) fetch_dy(dyn, c + 1);
         }
-        if (c + kBuf - 1 < nblk) issue(c + kBuf - 1);
-        const unsigned char* st = ring + (c % kBuf) * C::kStage;
-        const unsigned char* rec = st + C::kR;
-        const float* tab = reinterpret_cast<const float*>(rec + R::kTab);
+        if (c + kBuf - 1 < nblk) issue(c + kBuf - 1, (b + kBuf - 1) % kBuf);
+        const unsigned st = lds0 + b * C::kStage, rec = st + C::kR, tab = rec + R::kTab;
         const int rows = min(kDC, sq.len - c * kDC);
+
+        // what does not depend on the state first
+        Vec8<T> vf;
+        Pair<T> am[2], mm[2];
+        float gam8[8], del8[8], gt[2];
+        vtile_cols<C::kCV>(vf, st + C::kV, wave, r, g);
+        tab_rows(gam8, tab, g);
+        tab_rows(del8, tab + 128, g);
+        const float gl = lds_at<float>(tab + 124);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            load_pair(am[t], rrows, rec + R::kA, t);
+            if constexpr (kBwd) load_pair(mm[t], rrows, rec + R::kM, t); else rrows.load(mm[t].hi, rec + R::kM, t, 0);
+            gt[t] = lds_at<float>(tab + 4 * perm32(t, r));
+        }
 
         f32x4 ks[2], yt[2];
 #pragma unroll
@@ -158,87 +199,92 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 Vec8<T> kf, qf;
-                dtile_row<C::kCH>(kf, st + C::kK, 16 * t + r, kb, g);
+                krows.load(kf, st + C::kK, t, kb);
                 mma_xp(ks[t], kf, s);
-                dtile_row<C::kCH>(qf, st + C::kQ, 16 * t + r, kb, g);
+                krows.load(qf, st + C::kQ, t, kb);
                 if constexpr (kBwd) mma_px(yt[t], s, qf); else mma(yt[t], s.hi, qf);
             }
         }
-        // E = V - gam K S^T, rows past the sequence zero (their copies repeat the last row)
+        // E = V - gam K S^T (zero in rows past the sequence: their V and K are)
         float E[8];
-        {
-            Vec8<T> vf;
-            dtile_col<C::kCV>(vf, st + C::kV, 16 * wave, r, g);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int row = (i & 3) + 4 * g + (i >> 2) * 16;
-                E[i] = vf.get(i) - tab[row] * ks[i >> 2][i & 3];
-            }
-            if (rows < kDC) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) E[i] = (i & 3) + 4 * g + (i >> 2) * 16 < rows ? E[i] : 0.f;
-            }
-        }
+        for (int i = 0; i < 8; ++i) E[i] = vf.get(i) - gam8[i] * ks[i >> 2][i & 3];
         Pair<T> ep;
         ep.set(E);
-        float U[8], dU[8];
+        float e8[8], dU[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            Pair<T> a;
-            rec_rows(a, rec + R::kA, t, r, g);
-            f32x4 e = {0.f, 0.f, 0.f, 0.f};
-            mma_pp(e, a, ep);
+            f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
+            mma_pp(e, am[t], ep);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) {
-                const int row = 16 * t + 4 * g + m;
-                U[4 * t + m] = e[m] * tab[64 + row];
-                dU[4 * t + m] = U[4 * t + m] * tab[32 + row];
-            }
+            for (int m = 0; m < 4; ++m) e8[4 * t + m] = e[m];
             if constexpr (kBwd) {
                 // e once more with columns = tokens, the form in which it is kept
+                Vec8<T> one;
+                unit_frag(one, t, r, g);
                 f32x4 et = {0.f, 0.f, 0.f, 0.f};
-                mma_pp(et, ep, a);
-                store4(keep.e + keep.frag(sq.slot + c, h, pw / 16 + wave, d) + t * 256 + lane * 4, et[0], et[1], et[2], et[3]);
+                mma_pp(et, ep, am[t]);
+                mma_px(et, ep, one);
+                store4(keep.e + keep.frag(sq.slot + c, h, pw / 16 + wave, d) + keep.lane(perm32(t, r), g), et[0], et[1], et[2], et[3]);
             }
         }
+        // U = beta e (the forward's records have beta in M and in del)
+        if constexpr (kBwd) {
+            float be[8];
+            tab_rows(be, tab + 256, g);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) e8[i] *= be[i];
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) dU[i] = e8[i] * del8[i];
         Pair<T> du;
         du.set(dU);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) yt[t] *= tab[16 * t + r];
+        for (int t = 0; t < 2; ++t) yt[t] *= gt[t];
         if constexpr (kBwd) {
             Pair<T> up;
-            up.set(U);
+            up.set(e8);
+            // rows past the sequence are outside the buffer: dropped
+            const auto out = __builtin_amdgcn_make_buffer_rsrc(
+                keep.ydy + (pw / 16 + wave) * d.tokens * d.nheads + (sq.start + c * kDC) * d.nheads + h, 0,
+                (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                Pair<T> m;
-                rec_rows(m, rec + R::kM, t, r, g);
-                mma_pp(yt[t], up, m);
-                float dot = yt[t][0] * dyv[t].x + yt[t][1] * dyv[t].y + yt[t][2] * dyv[t].z + yt[t][3] * dyv[t].w;
+                mma_pp(yt[t], up, mm[t]);
+                float dot = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
                 dot += __shfl_xor(dot, 16, kWave);
                 dot += __shfl_xor(dot, 32, kWave);
-                if (g == 0 && 16 * t + r < rows)
-                    keep.ydy[(pw / 16 + wave) * d.tokens * d.nheads + (sq.start + c * kDC + 16 * t + r) * d.nheads + h] = dot;
+                // (the four lane groups hold the same sum)
+                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot), out, perm32(t, r) * (int)d.nheads * 4, 0, 0);
             }
         } else {
             Vec8<T> uf;
-            pack8(uf, U);
+            pack8(uf, e8);
+            const auto out = __builtin_amdgcn_make_buffer_rsrc(
+                y + ((sq.start + c * kDC) * d.nheads + h) * P + pw + 16 * wave, 0, (rows - 1) * (int)vrow + 16 * (int)sizeof(T),
+                kBufferDword3);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                Vec8<T> m;
-                dtile_row<kRecCH<T>>(m, rec + R::kM, 16 * t + r, 0, g);
-                mma(yt[t], uf, m);
-                if (16 * t + r < rows)
-                    store4(ybase + (int64_t)(c * kDC + 16 * t + r) * d.nheads * P + 4 * g, yt[t][0], yt[t][1],
-                           yt[t][2], yt[t][3]);
+                mma(yt[t], uf, mm[t].hi);
+                buffer_store4(out, perm32(t, r) * (int)vrow + 4 * g * (int)sizeof(T), 0, yt[t], T());
             }
         }
-        const float gl = tab[31];
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             S[t] *= gl;
             Vec8<T> kf;
-            dtile_col<C::kCH>(kf, st + C::kK, 16 * t, r, g);
+            kcols.load(kf, st + C::kK, t & 1, t >> 1);
             mma_xp(S[t], kf, du);
+        }
+    };
+    if constexpr (kBwd) {
+        if (nblk > 0) fetch_dy(dyn, 0);
+    }
+    for (int c = 0; c < nblk; c += kBuf) {
+        step(c, std::integral_constant<int, 0>());
+        if (c + 1 < nblk) step(c + 1, std::integral_constant<int, 1>());
+        if constexpr (kBuf > 2) {
+            if (c + 2 < nblk) step(c + 2, std::integral_constant<int, 2>());
         }
     }
     if constexpr (kBwd) {
@@ -246,8 +292,27 @@ __global__ __launch_bounds__(64 * NW) void delta_chain_kernel(
     } else {
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t)
-            if (16 * t < N) store4(fin + (sh * P + p) * N + 16 * t + 4 * g, S[t][0], S[t][1], S[t][2], S[t][3]);
+            if (ncol(t) < N) store4(fin + (sh * P + p) * N + ncol(t), S[t][0], S[t][1], S[t][2], S[t][3]);
     }
+}
+
+// With more than 256 registers at hand the compiler keeps S in accumulation registers, from where every scaling of it
+// takes two moves: the bf16 kernels are held to two wavefronts per SIMD, and their LDS is sized at the launch, so
+// that the compiler does not conclude from it that there is but one. The fp32 ones, whose fragments take
+// twice the registers, need the others.
+template <typename T, int NB, int NW, bool kBwd>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_chain_kernel(
+    const T* v, const T* Km, const T* Qm, const float* init, const unsigned char* recs, T* y, float* fin,
+    DeltaKeep<T> keep, DeltaDims d, int nslice)
+{
+    chain<T, NB, NW, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
+}
+template <typename T, int NB, int NW, bool kBwd>
+__global__ __launch_bounds__(64 * NW) void delta_chain_f32_kernel(
+    const T* v, const T* Km, const T* Qm, const float* init, const unsigned char* recs, T* y, float* fin,
+    DeltaKeep<T> keep, DeltaDims d, int nslice)
+{
+    chain<T, NB, NW, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
 }
 
 template <typename T, int NB, int NW, bool kBwd>
@@ -257,8 +322,14 @@ hipError_t launch_chain(const T* v, const T* k, const T* q, const float* init, c
     const int nslice = (int)d.headdim / (16 * NW);
     const int64_t nblocks = d.seqs * d.nheads * nslice;
     if (nblocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), 0, stream, v, k,
-                       q, init, rec, y, fin, keep, d, nslice);
+    using C = ChainCfg<T, NB, NW, kBwd>;
+    constexpr unsigned kLds = C::kBuf * C::kStage;
+    if constexpr (sizeof(T) == 2)
+        hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), kLds,
+                           stream, v, k, q, init, rec, y, fin, keep, d, nslice);
+    else
+        hipLaunchKernelGGL((delta_chain_f32_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), kLds,
+                           stream, v, k, q, init, rec, y, fin, keep, d, nslice);
     return hipGetLastError();
 }
 

@@ -25,7 +25,7 @@ __device__ __forceinline__ Vec8<T> load_row(const T* p, bool ok)
     return f;
 }
 
-// (I + L)^-1's column c, for strictly lower L in LDS (pitch kLd)
+// Column c of (I + L)^-1 - I, for strictly lower L in LDS (pitch kLd)
 __device__ __forceinline__ void unit_lower_column(float (&x)[32], const float* L, int c)
 {
 #pragma unroll
@@ -35,6 +35,8 @@ __device__ __forceinline__ void unit_lower_column(float (&x)[32], const float* L
         for (int j = 0; j < i; ++j) s = fmaf(-L[i * kLd + j], x[j], s);
         x[i] = s;
     }
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = i == c ? 0.f : x[i];
 }
 
 // Column c of a 32 x 32 matrix into a record's tile(s): T, or with kPairs a hi and a lo plane.
@@ -43,7 +45,7 @@ __device__ __forceinline__ void put_column(unsigned char* m, const float (&x)[32
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        unsigned char* at = m + DTile<4>::offset(i, c >> 3) + 2 * (c & 7);
+        unsigned char* at = m + WTile<4>::offset(i, c >> 3) + 2 * (c & 7);
         const bf16 hi = static_cast<bf16>(x[i]);
         *reinterpret_cast<bf16*>(at) = hi;
         if constexpr (kPairs) *reinterpret_cast<bf16*>(at + 2048) = static_cast<bf16>(x[i] - static_cast<float>(hi));
@@ -54,7 +56,7 @@ __device__ __forceinline__ void put_column(unsigned char* m, const float (&x)[32
 {
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        *reinterpret_cast<float*>(m + DTile<8>::offset(i, c >> 2) + 4 * (c & 3)) = x[i];
+        *reinterpret_cast<float*>(m + WTile<8>::offset(i, c >> 2) + 4 * (c & 3)) = x[i];
 }
 
 // kHeads heads of one group and block: a wavefront for every two
@@ -129,7 +131,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(
     for (int i = 0; i < 32; ++i) {
         const float G = __expf((float)(css[hw][i] - cs));
         const bool ok = tok && i < rows;
-        M[i] = ok && i >= c ? G * qk[i * kLd + c] : 0.f;
+        M[i] = ok && i >= c ? G * qk[i * kLd + c] * (kBwd ? 1.f : be) : 0.f;
         L[i * kLd + c] = ok && i > c ? G * kk[i * kLd + c] * be : 0.f;
     }
     float x[32];
@@ -152,7 +154,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(
     }
     float* tab = reinterpret_cast<float*>(B + R::kTab);
     tab[c] = __expf((float)cs);
-    tab[32 + c] = __expf((float)(css[hw][31] - cs));
+    tab[32 + c] = __expf((float)(css[hw][31] - cs)) * (kBwd ? 1.f : be);
     tab[64 + c] = be;
     tab[96 + c] = 0.f;
     asm volatile("" ::: "memory");
