@@ -34,9 +34,8 @@ constexpr int kChunk = 64;       // tokens of a chunk of the dq, dk step
 // What the walk back keeps, beside DeltaKeep.
 template <typename T> struct DeltaBack {
     T* w;                    // as e: w of every block, head and 16 columns
-    float* vdv;              // (headdim / 16, tokens, nheads): dv . v over 16 columns
-    float* we;               // the same of w . e
-    T* H;                    // (seqs, chunks, nheads, headdim, dstate): dL/d(state after each 64-token chunk)
+    float* sums;             // (headdim / 16, seqs, nheads, 2, 64 chunks): dv . v and w . e over 16 columns
+    T* H;                    // (seqs, chunks, nheads): dL/d(state after each 64-token chunk), as fragments
     float* hs;               // (headdim / 16, seqs, chunks + 1, nheads): <H, S> over 16 rows at the chunks' ends
 };
 
@@ -142,16 +141,16 @@ __device__ __forceinline__ void walk_back(
     // allow, it is fetched a block ahead.
     constexpr bool kAhead = NB * sizeof(T) <= 8;
     typedef decltype(load_raw(static_cast<const T*>(nullptr))) Raw;
-    Raw shi[kAhead ? 2 * NB : 1], slo[kAhead && sizeof(T) == 2 ? 2 * NB : 1];
-    auto at_S = [&](int k) { return ((s * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N; };
+    Vec8<T> shi[kAhead ? NB : 1], slo[kAhead && sizeof(T) == 2 ? NB : 1];
+    auto at_S = [&](int k) { return keep.state_at((s * (keep.chunks + 1) + k) * d.nheads + h, pt, lane, d); };
     auto fetch_S = [&](int k) __attribute__((always_inline)) {
         if constexpr (kAhead) {
             const int64_t at = at_S(k);
 #pragma unroll
-            for (int t = 0; t < 2 * NB; ++t) {
-                if (ncol(t) < N) {
-                    shi[t] = load_raw(keep.S + at + ncol(t));
-                    if constexpr (sizeof(T) == 2) slo[t] = load_raw(keep.Slo + at + ncol(t));
+            for (int kb = 0; kb < NB; ++kb) {
+                if (32 * kb < N) {
+                    load8(shi[kb], keep.S + at + kb * keep.kb_stride);
+                    if constexpr (sizeof(T) == 2) load8(slo[kb], keep.Slo + at + kb * keep.kb_stride);
                 }
             }
         }
@@ -160,13 +159,17 @@ __device__ __forceinline__ void walk_back(
         const int64_t at = at_S(k);
         float dot = 0.f;
 #pragma unroll
-        for (int t = 0; t < 2 * NB; ++t) {
-            if (ncol(t) < N) {
-                const f32x4 a = raw_f32(kAhead ? shi[kAhead ? t : 0] : load_raw(keep.S + at + ncol(t)));
-                dot += H[t][0] * a[0] + H[t][1] * a[1] + H[t][2] * a[2] + H[t][3] * a[3];
+        for (int kb = 0; kb < NB; ++kb) {
+            if (32 * kb < N) {
+                Vec8<T> a, l;
+                if constexpr (kAhead) a = shi[kb]; else load8(a, keep.S + at + kb * keep.kb_stride);
                 if constexpr (sizeof(T) == 2) {
-                    const f32x4 l = raw_f32(kAhead ? slo[kAhead ? t : 0] : load_raw(keep.Slo + at + ncol(t)));
-                    dot += H[t][0] * l[0] + H[t][1] * l[1] + H[t][2] * l[2] + H[t][3] * l[3];
+                    if constexpr (kAhead) l = slo[kb]; else load8(l, keep.Slo + at + kb * keep.kb_stride);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    dot = fmaf(H[2 * kb + (i >> 2)][i & 3], a.get(i), dot);
+                    if constexpr (sizeof(T) == 2) dot = fmaf(H[2 * kb + (i >> 2)][i & 3], l.get(i), dot);
                 }
             }
         }
@@ -196,15 +199,22 @@ __device__ __forceinline__ void walk_back(
     auto step = [&](int c, auto stage) __attribute__((always_inline)) {
         constexpr int b = decltype(stage)::value;
         // (see the walk forward; the loads ahead of the next block were started before its copies)
-        constexpr int kStores = 8;
+        constexpr int kStores = 5;
         if (c < nblk - 1) wait_vmem_below<kStores>(); else wait_vmem();
         __syncthreads();
         if (c % 2 == 1 || c == nblk - 1) {
             const int k = c / 2;
-            const int64_t at = ((s * keep.chunks + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
+            const int64_t at = keep.state_at((s * keep.chunks + k) * d.nheads + h, pt, lane, d);
 #pragma unroll
-            for (int t = 0; t < 2 * NB; ++t)
-                if (ncol(t) < N) store4(back.H + at + ncol(t), H[t][0], H[t][1], H[t][2], H[t][3]);
+            for (int kb = 0; kb < NB; ++kb) {
+                if (32 * kb < N) {
+                    const float hv[8] = {H[2 * kb][0], H[2 * kb][1], H[2 * kb][2], H[2 * kb][3],
+                                         H[2 * kb + 1][0], H[2 * kb + 1][1], H[2 * kb + 1][2], H[2 * kb + 1][3]};
+                    Vec8<T> hf;
+                    pack8(hf, hv);
+                    store8(back.H + at + kb * keep.kb_stride, hf);
+                }
+            }
             put_inner(k + 1);
         }
         if (c % 2 == 0) fetch_S(c / 2);
@@ -268,8 +278,7 @@ __device__ __forceinline__ void walk_back(
         // sequence are outside the buffers: dropped.
         const int64_t th = (sq.start + c * kDC) * d.nheads + h;
         const auto odv = __builtin_amdgcn_make_buffer_rsrc(dv + th * P + 16 * pt, 0, (rows - 1) * (int)vrow + 16 * (int)sizeof(T), kBufferDword3);
-        const auto ovd = __builtin_amdgcn_make_buffer_rsrc(back.vdv + pt * d.tokens * d.nheads + th, 0, (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
-        const auto owe = __builtin_amdgcn_make_buffer_rsrc(back.we + pt * d.tokens * d.nheads + th, 0, (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
+        float we[2], vd[2];
         float bw[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
@@ -282,20 +291,15 @@ __device__ __forceinline__ void walk_back(
 #pragma unroll
             for (int m = 0; m < 4; ++m) bw[4 * t + m] = -ga[4 * t + m] * bt8[4 * t + m] * w[m];
             store4(back.w + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g), wt[0], wt[1], wt[2], wt[3]);
-            float we = wt[0] * ev[t][0] + wt[1] * ev[t][1] + wt[2] * ev[t][2] + wt[3] * ev[t][3];
+            we[t] = wt[0] * ev[t][0] + wt[1] * ev[t][1] + wt[2] * ev[t][2] + wt[3] * ev[t][3];
             wt *= bet[t];
             const f32x4 vf = raw_f32(vv[t]);
-            float vd = wt[0] * vf[0] + wt[1] * vf[1] + wt[2] * vf[2] + wt[3] * vf[3];
-            we += __shfl_xor(we, 16, kWave);
-            vd += __shfl_xor(vd, 16, kWave);
-            we += __shfl_xor(we, 32, kWave);
-            vd += __shfl_xor(vd, 32, kWave);
-            const int tok = perm32(t, r);
-            buffer_store4(odv, tok * (int)vrow + 4 * g * (int)sizeof(T), 0, wt, T());
-            // (the four lane groups hold the same sums)
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(vd), ovd, tok * (int)d.nheads * 4, 0, 0);
-            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(we), owe, tok * (int)d.nheads * 4, 0, 0);
+            vd[t] = wt[0] * vf[0] + wt[1] * vf[1] + wt[2] * vf[2] + wt[3] * vf[3];
+            buffer_store4(odv, perm32(t, r) * (int)vrow + 4 * g * (int)sizeof(T), 0, wt, T());
         }
+        // lane group g: dv . v (g even) or w . e of tile g / 2
+        back.sums[(((pt * d.seqs + s) * d.nheads + h) * 2 + (g & 1)) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
+            sum_groups(vd[0], vd[1], we[0], we[1]);
         // H before the block = gam_last H + Q^T (gam dY) - K^T (beta gam w)
         float gy[8];
 #pragma unroll
@@ -341,62 +345,53 @@ __global__ __launch_bounds__(64 * NW) void delta_rev_f32_kernel(
 
 // ---- dbeta and dg ---------------------------------------------------------------------------------------------
 
-// A workgroup = two 64-token chunks x 64 heads: a wavefront sums 32 tokens, a lane one head.
+// A wavefront = one 64-token chunk of one head, lane = token; a workgroup = that chunk of 16 heads, whose results are
+// turned in LDS so that they leave as pieces of token rows.
 __global__ __launch_bounds__(256) void delta_scalar_kernel(
-    const float* __restrict__ ydy, const float* __restrict__ vdv, const float* __restrict__ we,
-    const float* __restrict__ hs, float* __restrict__ dg, float* __restrict__ dbeta, DeltaDims d, int64_t chunks,
-    int nseg, int hblocks, int zero_first)
+    const float* __restrict__ ydy, const float* __restrict__ sums, const float* __restrict__ hs, float* __restrict__ dg,
+    float* __restrict__ dbeta, DeltaDims d, int64_t chunks, int hblocks, int zero_first)
 {
-    __shared__ double part[4][64];
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
-    const int hb = blockIdx.x % hblocks;
-    const int seg = (blockIdx.x / hblocks) % nseg;
-    const int64_t s = blockIdx.x / hblocks / nseg;
-    const int h = hb * 64 + lane;
-    const bool live = h < d.nheads;
+    __shared__ float og[64][17], ob[64][17];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    const int h0 = (int)(blockIdx.x % hblocks) * 16;
+    const int64_t sk = blockIdx.x / hblocks, s = sk / chunks, k = sk % chunks;
+    const int left = (int)min(d.seqlen - 64 * k, (int64_t)64);
     const int npt = (int)d.headdim / 16;
-    const int64_t TH = d.tokens * d.nheads;
-    const int t0 = seg * 128 + 32 * wave;
-    float loc[32];
-#pragma unroll
-    for (int i = 0; i < 32; ++i) {
-        loc[i] = 0.f;
-        if (live && t0 + i < d.seqlen) {
-            const int64_t th = (s * d.seqlen + t0 + i) * d.nheads + h;
-            float b = 0.f;
-            for (int pt = 0; pt < npt; ++pt) {
-                loc[i] += ydy[pt * TH + th] - vdv[pt * TH + th];
-                b += we[pt * TH + th];
+    for (int i = wave; i < 16; i += 4) {
+        const int h = h0 + i;
+        if (h >= d.nheads) break;
+        float loc = 0.f, b = 0.f;
+        double start = 0.0, end = 0.0;
+        for (int pt = 0; pt < npt; ++pt) {
+            const int64_t row = (pt * d.seqs + s) * d.nheads + h;
+            if (lane < left) {
+                const float* at = sums + row * 2 * chunks * 64 + k * 64 + lane;
+                loc += ydy[row * chunks * 64 + k * 64 + lane] - at[0];
+                b += at[chunks * 64];
             }
-            dbeta[th] = b;
+            const float* e = hs + ((pt * d.seqs + s) * (chunks + 1) + k) * d.nheads + h;
+            start += e[0];
+            end += e[d.nheads];
         }
-    }
-    double sum = 0.0;
+        // sums from this token to the chunk's end
+        double run = loc;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) sum += loc[i];
-    part[wave][lane] = sum;
+        for (int m = 1; m < 64; m <<= 1) {
+            const double down = __shfl_down(run, m, 64);
+            if (lane + m < 64) run += down;
+        }
+        const double miss = (start - end - __shfl(run, 0, 64)) / left;
+        og[lane][i] = (float)(end + run + miss * (left - lane));
+        ob[lane][i] = b;
+    }
     __syncthreads();
-    if (!live) return;
-    const int64_t k = 2 * seg + (wave >> 1);
-    const int left = (int)d.seqlen - 64 * (int)k;           // tokens from the chunk's start on
-    if (left <= 0) return;
-    double run = 0.0, start = 0.0;
-    for (int pt = 0; pt < npt; ++pt) {
-        const float* at = hs + ((pt * d.seqs + s) * (chunks + 1) + k) * d.nheads + h;
-        start += at[0];
-        run += at[d.nheads];
-    }
-    const double miss = (start - run - part[wave & 2][lane] - part[(wave & 2) + 1][lane]) / min(left, 64);
-    if (!(wave & 1)) {
-        run += part[wave + 1][lane];
-        if (left > 32) run += miss * (min(left, 64) - 32);
-    }
-#pragma unroll
-    for (int i = 31; i >= 0; --i) {
-        if (t0 + i < d.seqlen) {
-            run += loc[i] + miss;
+    for (int j = threadIdx.x; j < 1024; j += 256) {
+        const int t = j / 16, i = j % 16;
+        if (t < left && h0 + i < d.nheads) {
+            const int64_t at = (s * d.seqlen + k * 64 + t) * d.nheads + h0 + i;
             // without an initial state nothing decays into the first token
-            dg[(s * d.seqlen + t0 + i) * d.nheads + h] = zero_first && t0 + i == 0 ? 0.f : (float)run;
+            dg[at] = zero_first && k == 0 && t == 0 ? 0.f : og[t][i];
+            dbeta[at] = ob[t][i];
         }
     }
 }
@@ -447,8 +442,28 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
     const bool tok = mine < rows;
     const unsigned lds0 = lds_addr(&ring[0]);
     const DCols<T, C::kCH> cols(r, g);
-    DTileCopy<C::kCH, 4> scopy;
-    scopy.plan((unsigned)(N * sizeof(T)), wave, lane);
+    // 32 rows of a kept state (two 16-row pieces of fragments) into a tile
+    constexpr int kIs = DTile<C::kCH>::kInst, kKs = (kIs + 3) / 4;
+    const int nkc = (N + 31) / 32;
+    auto copy_state = [&](const T* m, int rows, unsigned lds) __attribute__((always_inline)) {
+#pragma unroll
+        for (int q4 = 0; q4 < kKs; ++q4) {
+            const int q = wave + 4 * q4;
+            if (kIs % 4 != 0 && q >= kIs) break;
+            int rr, c;
+            DTileCopy<C::kCH, 4>::place(q, lane, rr, c);
+            // chunk c: 16 / sizeof(T) of the columns 8 gc .. 8 gc + 7 of the 32 numbered kc
+            constexpr int kPer = 8 * (int)sizeof(T) / 16;
+            const int kc = c / (4 * kPer), gc = c / kPer % 4, part = c % kPer;
+            const unsigned off = (unsigned)(((rr >> 4) * nkc + kc) * 512 + (16 * gc + (rr & 15)) * 8) * (unsigned)sizeof(T) + 16u * part;
+            if (c < valid) {
+                if (rr < rows)
+                    dma16_at(m, off, lds + q * 1024u);
+                else
+                    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(lds + q * 1024u + lane * 16u) = u32x4{0, 0, 0, 0};
+            }
+        }
+    };
 
     auto zero_pad = [&](int tiles) {
         for (int i = threadIdx.x; i < tiles * 32 * C::kCH; i += 256) {
@@ -466,11 +481,9 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
         const int h = h0 + i / nkb, kb = i % nkb;
         const unsigned st = lds0 + (unsigned)(i & 1) * C::kStage;
         const int rows = P - 32 * kb;
-        const int64_t pn = (int64_t)P * N, off = (int64_t)32 * kb * N;
-        scopy.issue(keep.S + ((s * (keep.chunks + 1) + k) * d.nheads + h) * pn + off, (unsigned)(N * sizeof(T)), rows,
-                    valid, st, wave, lane);
-        scopy.issue(back.H + ((s * keep.chunks + k) * d.nheads + h) * pn + off, (unsigned)(N * sizeof(T)), rows, valid,
-                    st + C::kTile, wave, lane);
+        const int64_t off = (int64_t)2 * kb * nkc * 512;
+        copy_state(keep.S + ((s * (keep.chunks + 1) + k) * d.nheads + h) * keep.plane(d) + off, rows, st);
+        copy_state(back.H + ((s * keep.chunks + k) * d.nheads + h) * keep.plane(d) + off, rows, st + C::kTile);
     };
     // the operands of a stage in registers: lane = token, slots = columns {4g .., 16 + 4g ..} of 32
     struct Ops { float4 y[2], e[2], w[2]; float gr, be; };
@@ -681,12 +694,12 @@ int kq_slices(const DeltaDims& d)
     return (int)(want < hpg / 2 ? want : hpg / 2 > 1 ? hpg / 2 : 1);
 }
 
-struct BwdSpace { size_t rec, e, w, ydy, vdv, we, S, Slo, H, hs, part, total; };
+struct BwdSpace { size_t rec, e, w, ydy, sums, S, Slo, H, hs, part, total; };
 
 BwdSpace bwd_space(const DeltaDims& d, size_t es)
 {
     const size_t chunks = (d.seqlen + kChunk - 1) / kChunk, slots = delta_slots(d), heads = d.nheads;
-    const size_t npt = d.headdim / 16, pn = d.headdim * d.dstate, th = (size_t)d.tokens * heads;
+    const size_t npt = d.headdim / 16, pn = d.headdim * ((d.dstate + 31) / 32 * 32), th = (size_t)d.seqs * heads * chunks * 64;
     const int ns = kq_slices(d);
     BwdSpace b;
     size_t at = 0;
@@ -695,8 +708,7 @@ BwdSpace bwd_space(const DeltaDims& d, size_t es)
     b.e = put(slots * heads * npt * 512 * 4);
     b.w = put(slots * heads * npt * 512 * es);
     b.ydy = put(npt * th * 4);
-    b.vdv = put(npt * th * 4);
-    b.we = put(npt * th * 4);
+    b.sums = put(npt * th * 2 * 4);
     b.S = put((size_t)d.seqs * (chunks + 1) * heads * pn * es);
     b.Slo = put(es == 2 ? (size_t)d.seqs * (chunks + 1) * heads * pn * es : 0);
     b.H = put((size_t)d.seqs * chunks * heads * pn * es);
@@ -764,7 +776,7 @@ hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, 
     auto t = [&](size_t at) { return reinterpret_cast<T*>(ws + at); };
     const int64_t chunks = (d.seqlen + kChunk - 1) / kChunk;
     const DeltaKeep<T> keep{dy, f(b.e), f(b.ydy), t(b.S), t(b.Slo), chunks};
-    const DeltaBack<T> back{t(b.w), f(b.vdv), f(b.we), t(b.H), f(b.hs)};
+    const DeltaBack<T> back{t(b.w), f(b.sums), t(b.H), f(b.hs)};
     hipError_t e = launch_delta_prep<T, true>(k, q, g, beta, ws + b.rec, d, stream);
     if (e == hipSuccess)
         e = launch_delta_chain<T, true>(v, k, q, init, ws + b.rec, nullptr, nullptr, keep, d, stream);
@@ -778,9 +790,9 @@ hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, 
     else
         e = launch_nb<T, 8>(v, g, beta, k, q, dfinal, ws + b.rec, dv, dk, dq, dinit, f(b.part), keep, back, d, stream);
     if (e != hipSuccess || d.seqlen == 0) return e;
-    const int nseg = (int)((d.seqlen + 127) / 128), hblocks = (int)((d.nheads + 63) / 64);
-    hipLaunchKernelGGL(delta_scalar_kernel, dim3((unsigned)(d.seqs * nseg * hblocks)), dim3(256), 0, stream, keep.ydy,
-                       back.vdv, back.we, back.hs, dg, dbeta, d, chunks, nseg, hblocks, init == nullptr ? 1 : 0);
+    const int hblocks = (int)((d.nheads + 15) / 16);
+    hipLaunchKernelGGL(delta_scalar_kernel, dim3((unsigned)(d.seqs * chunks * hblocks)), dim3(256), 0, stream, keep.ydy,
+                       back.sums, back.hs, dg, dbeta, d, chunks, hblocks, init == nullptr ? 1 : 0);
     return hipGetLastError();
 }
 

@@ -126,17 +126,16 @@ __device__ __forceinline__ void chain(
 
     // the state entering a chunk of 64 tokens (k = 0 ..) and after the last one
     auto keep_state = [&](int k) __attribute__((always_inline)) {
-        const int64_t at = (((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h) * (int64_t)P * N + (int64_t)p * N;
+        const int64_t at = keep.state_at(((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h, pw / 16 + wave, lane, d);
 #pragma unroll
-        for (int t = 0; t < 2 * NB; ++t) {
-            if (ncol(t) < N) {
-                store4(keep.S + at + ncol(t), S[t][0], S[t][1], S[t][2], S[t][3]);
-                if (sizeof(T) == 2) {
-                    float lo[4];
-#pragma unroll
-                    for (int m = 0; m < 4; ++m) lo[m] = S[t][m] - to_f32(from_f32<T>(S[t][m]));
-                    store4(keep.Slo + at + ncol(t), lo[0], lo[1], lo[2], lo[3]);
-                }
+        for (int kb = 0; kb < NB; ++kb) {
+            if (32 * kb < N) {
+                const float sv[8] = {S[2 * kb][0], S[2 * kb][1], S[2 * kb][2], S[2 * kb][3],
+                                     S[2 * kb + 1][0], S[2 * kb + 1][1], S[2 * kb + 1][2], S[2 * kb + 1][3]};
+                Pair<T> s;
+                s.set(sv);
+                store8(keep.S + at + kb * keep.kb_stride, s.hi);
+                if constexpr (sizeof(T) == 2) store8(keep.Slo + at + kb * keep.kb_stride, s.lo);
             }
         }
     };
@@ -156,7 +155,7 @@ __device__ __forceinline__ void chain(
         constexpr int b = decltype(stage)::value;
         // This stage's copies are done when what was started after them is all that is outstanding (the counter goes
         // down in order): the later stages' copies and the last block's kStores stores.
-        constexpr int kStores = kBwd ? 4 : 2;
+        constexpr int kStores = kBwd ? 3 : 2;
         constexpr int kLater = (kBuf - 2) * C::kMin < 63 - kStores ? (kBuf - 2) * C::kMin : 63 - kStores;
         if (c + kBuf - 2 >= nblk) wait_vmem();
         else if (c > 0) wait_vmem_below<kLater + kStores>();
@@ -244,19 +243,15 @@ __device__ __forceinline__ void chain(
         if constexpr (kBwd) {
             Pair<T> up;
             up.set(e8);
-            // rows past the sequence are outside the buffer: dropped
-            const auto out = __builtin_amdgcn_make_buffer_rsrc(
-                keep.ydy + (pw / 16 + wave) * d.tokens * d.nheads + (sq.start + c * kDC) * d.nheads + h, 0,
-                (rows - 1) * (int)d.nheads * 4 + 4, kBufferDword3);
+            float dot[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 mma_pp(yt[t], up, mm[t]);
-                float dot = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
-                dot += __shfl_xor(dot, 16, kWave);
-                dot += __shfl_xor(dot, 32, kWave);
-                // (the four lane groups hold the same sum)
-                __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(dot), out, perm32(t, r) * (int)d.nheads * 4, 0, 0);
+                dot[t] = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
             }
+            // (32 tokens as 2 x 64 bytes, each twice; what is past the sequence is not read)
+            keep.ydy[(((pw / 16 + wave) * d.seqs + sh / d.nheads) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
+                sum_groups(dot[0], dot[1]);
         } else {
             Vec8<T> uf;
             pack8(uf, e8);

@@ -429,9 +429,9 @@ __device__ __forceinline__ void tab_rows(float (&v)[8], unsigned tab, int g)
 template <typename T> struct DeltaKeep {
     const T* dy;
     float* e;                // e of every block, head and 16 columns: (2 x 16 tokens) as 64 lanes (4 columns, token) x 4
-    float* ydy;              // (headdim / 16, tokens, nheads): dy . y over 16 columns
-    T* S;                    // (seqs, chunks + 1, nheads, headdim, dstate): the state entering each 64-token chunk,
-    T* Slo;                  //   and after the last; for bf16 also what the rounding to T drops
+    float* ydy;              // (headdim / 16, seqs, nheads, 64 chunks): dy . y over 16 columns
+    T* S;                    // (seqs, chunks + 1, nheads): the state entering each 64-token chunk, and after the last, as
+    T* Slo;                  //   fragments (state_at); for bf16 also what the rounding to T drops
     int64_t chunks;          // 64-token chunks of a row
     __device__ __forceinline__ int64_t frag(int64_t slot, int h, int pt, const DeltaDims& d) const
     {
@@ -439,7 +439,37 @@ template <typename T> struct DeltaKeep {
     }
     // where token i of the 32 has its columns 4g .. 4g + 3
     __device__ __forceinline__ static int lane(int i, int g) { return (i >> 4) * 256 + (16 * g + (i & 15)) * 4; }
+    // Plane k of a kept state: per 16 rows p and 32 columns n, 64 lanes (g, p) x columns 8g .. 8g + 7, so that
+    // a walk's stores and loads are whole lines. kb_stride elements from one 32 columns to the next.
+    static constexpr int kb_stride = 512;
+    __device__ __forceinline__ static int64_t plane(const DeltaDims& d)
+    {
+        return d.headdim * ((d.dstate + 31) / 32 * 32);
+    }
+    __device__ __forceinline__ static int64_t state_at(int64_t plane_index, int pt, int lane_id, const DeltaDims& d)
+    {
+        return plane_index * plane(d) + (int64_t)pt * ((d.dstate + 31) / 32) * kb_stride + lane_id * 8;
+    }
 };
+
+// Sums over the four lane groups of two values at once: lane group g returns the sum of a (g < 2) or b (g >= 2) at its
+// own r.
+__device__ __forceinline__ float sum_groups(float a, float b)
+{
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    const float s = __uint_as_float(x[0]) + __uint_as_float(x[1]);
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(s), false, false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+}
+// The same of four: lane group g returns the sum of a (0), c (1), b (2), d (3).
+__device__ __forceinline__ float sum_groups(float a, float b, float c, float d)
+{
+    const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(b), false, false);
+    const auto z = __builtin_amdgcn_permlane32_swap(__float_as_uint(c), __float_as_uint(d), false, false);
+    const float s = __uint_as_float(x[0]) + __uint_as_float(x[1]), t = __uint_as_float(z[0]) + __uint_as_float(z[1]);
+    const auto y = __builtin_amdgcn_permlane16_swap(__float_as_uint(s), __float_as_uint(t), false, false);
+    return __uint_as_float(y[0]) + __uint_as_float(y[1]);
+}
 
 template <typename T, bool kBwd>
 hipError_t launch_delta_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
