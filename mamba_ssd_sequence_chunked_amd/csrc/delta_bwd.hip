@@ -574,6 +574,7 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
                 mma(za[t], wf, u);
             }
         }
+        settle();
         if (kb == nkb - 1) {
             // the head's W and Z, rows i = 16 wave + 4g + m, columns j = 16 t + r
 #pragma unroll
@@ -649,6 +650,7 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
             mma(ak[t], qf, wc);
         }
     }
+    settle();
     if (!tok) return;
     const int64_t at = ((t0 + mine) * d.ngroups + grp) * N + 4 * g;
     const int64_t all = d.tokens * d.ngroups * N;

@@ -15,8 +15,13 @@
 // kBwd is the backward's walk forward: the same block by block, with y kept to fp32's accuracy (pairs there too)
 // and, in place of y and the final state, what the walk back and the gradients of k and q need (DeltaKeep).
 //
-// A workgroup = NW wavefronts = 16 NW rows of one (sequence, head).  K, Q, the V columns and the block's record come
-// through a ring of NBUF stages of asynchronous global -> LDS copies; one barrier per block.
+// A workgroup = NW wavefronts that walk (16 rows each, of one head or of NH next to each other) and one that feeds
+// them: K, Q, the V columns and the blocks' records come through a ring of kBuf stages of asynchronous global -> LDS
+// copies, all issued by that one. A wavefront that issues copies stalls while they queue up (28 KB a block at 64
+// bytes a cycle), which cost the walk a fifth of its time when its own wavefronts did (192 heads of 64 x 128 over
+// 2048 tokens: 74 us against 91). One barrier per block.
+// What bounds it: the chain of one block's products, about 2700 cycles of which a wavefront's matrix instructions
+// fill 770 and its vector instructions 880; two wavefronts on a SIMD take 4200 a block.
 #include <type_traits>
 
 #include "delta_tiles.hpp"
@@ -25,61 +30,60 @@ namespace ssd {
 
 namespace {
 
-template <typename T, int NB, int NW, bool kBwd>
+template <typename T, int NB, int NW, int NH, bool kBwd>
 struct ChainCfg {
     using R = DeltaRec<T, kBwd>;
     static constexpr int kCH = NB * 32 * (int)sizeof(T) / 16;      // chunks of a K or Q row
     static constexpr int kCV = 16 * NW * (int)sizeof(T) / 16;      // chunks of a V row
     static constexpr int kK = 0, kQ = DTile<kCH>::kBytes, kV = 2 * DTile<kCH>::kBytes,
                          kR = kV + DTile<kCV>::kBytes;
-    static constexpr int kStage = kR + R::kFwdBytes;
-    static constexpr int kRecInst = (R::kFwdBytes + 1023) / 1024;
-    // copies every wavefront makes per stage, at least
-    static constexpr int kMin = 2 * (DTile<kCH>::kInst / NW) + DTile<kCV>::kInst / NW + kRecInst / NW;
-    static constexpr int kBuf = 3 * kStage <= 80 * 1024 ? 3 : 2 * kStage <= 160 * 1024 ? 2 : 1;
+    static constexpr int kStage = kR + NH * R::kFwdBytes;
+    // copies of a stage, each of 1 KB
+    static constexpr int kCopies = 2 * DTile<kCH>::kInst + DTile<kCV>::kInst + NH * ((R::kFwdBytes + 1023) / 1024);
+    // (a third stage of the largest tiles costs registers, and with them a tenth of the time)
+    static constexpr int kBuf = 3 * kStage <= (NW > 4 ? 160 : 80) * 1024 ? 3 : 2;
+    static constexpr int kLds = kBuf * kStage;
 };
 
-template <typename T, int NB, int NW, bool kBwd>
+template <typename T, int NB, int NW, int NH, bool kBwd>
 __device__ __forceinline__ void chain(
     const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ init,
     const unsigned char* __restrict__ recs, T* __restrict__ y, float* __restrict__ fin, DeltaKeep<T> keep, DeltaDims d,
     int nslice)
 {
-    using C = ChainCfg<T, NB, NW, kBwd>;
+    using C = ChainCfg<T, NB, NW, NH, kBwd>;
     using R = DeltaRec<T, kBwd>;
     constexpr int kBuf = C::kBuf;
-    static_assert(kBuf >= 2 && kBuf * C::kStage <= 160 * 1024, "ring");
-    extern __shared__ __attribute__((aligned(1024))) unsigned char ring[];        // kBuf * C::kStage
+    static_assert(C::kLds <= 160 * 1024, "ring");
+    extern __shared__ __attribute__((aligned(1024))) unsigned char ring[];        // C::kLds
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
     const int bid = xcd_logical_block(blockIdx.x, gridDim.x);
     const int slice = bid % nslice;
-    const int64_t sh = bid / nslice;
-    const int h = (int)(sh % d.nheads);
-    const DeltaSeq sq = delta_seq(d, sh / d.nheads);
-    const int grp = h / (int)(d.nheads / d.ngroups);
+    const int64_t sh0 = bid / nslice * NH;
+    const int h0 = (int)(sh0 % d.nheads);                 // the workgroup's (first) head
+    const DeltaSeq sq = delta_seq(d, sh0 / d.nheads);
+    const int grp = h0 / (int)(d.nheads / d.ngroups);
     const int N = (int)d.dstate, P = (int)d.headdim;
-    const int pw = 16 * NW * slice;                       // the workgroup's first column of v
-    const int p = pw + 16 * wave + r;                     // this lane's column
+    const int pw = 16 * (NW / NH) * slice;                // the workgroup's first column of v
+    const int hw = wave / (NW / NH), h = h0 + hw;         // this wavefront's head
+    const int64_t sh = sh0 + hw;
+    const int pv = pw + 16 * (wave % (NW / NH));          // and first column
     const int nblk = (sq.len + kDC - 1) / kDC;
     const int valid = N * (int)sizeof(T) / 16;
 
     const unsigned krow = (unsigned)(d.ngroups * N * sizeof(T)), vrow = (unsigned)(d.nheads * P * sizeof(T));
     const T* kbase = Km + (sq.start * d.ngroups + grp) * N;
     const T* qbase = Qm + (sq.start * d.ngroups + grp) * N;
-    const T* vbase = v + (sq.start * d.nheads + h) * P + pw;
-    const unsigned char* rbase = recs + (sq.slot * d.nheads + h) * (int64_t)R::kBytes;
+    const T* vbase = v + (sq.start * d.nheads + h0) * P + pw;
+    const unsigned char* rbase = recs + (sq.slot * d.nheads + h0) * (int64_t)R::kBytes;
     const unsigned lds0 = lds_addr(&ring[0]);
     const WRows<T, C::kCH> krows(r, g);
     const WCols<T, C::kCH> kcols(r, g);
     const WRows<T, kRecCH<T>> rrows(r, g);
-    DTileCopy<C::kCH, NW, WTile<C::kCH>> kcopy;
-    DTileCopy<C::kCV, NW, VTile<C::kCV>> vcopy;
-    kcopy.plan(krow, wave, lane);
-    vcopy.plan(vrow, wave, lane);
 
     if (valid < C::kCH) {
         // columns past N are never copied: zero them once, so that the state's rows there stay zero
-        for (int i = threadIdx.x; i < kBuf * 32 * C::kCH; i += 64 * NW) {
+        for (int i = threadIdx.x; i < kBuf * 32 * C::kCH; i += 64 * (NW + 1)) {
             const int row = (i / C::kCH) % 32, b = i / (32 * C::kCH), c = i % C::kCH;
             if (c >= valid) {
                 unsigned char* st = ring + b * C::kStage + WTile<C::kCH>::offset(row, c);
@@ -90,85 +94,83 @@ __device__ __forceinline__ void chain(
         __syncthreads();
     }
 
-    // the copies of block c (called in order) into stage b
-    const unsigned char* kp = reinterpret_cast<const unsigned char*>(kbase);
-    const unsigned char* qp = reinterpret_cast<const unsigned char*>(qbase);
-    const unsigned char* vp = reinterpret_cast<const unsigned char*>(vbase);
-    const unsigned char* rp = rbase;
-    auto issue = [&](int c, int b) __attribute__((always_inline)) {
-        const unsigned st = lds0 + (unsigned)b * C::kStage;
-        const int rows = sq.len - c * kDC;
-        kcopy.issue(kp, krow, rows, valid, st + C::kK, wave, lane);
-        kcopy.issue(qp, krow, rows, valid, st + C::kQ, wave, lane);
-        vcopy.issue(vp, vrow, rows, C::kCV, st + C::kV, wave, lane);
-        linear_copy<R::kFwdBytes, NW>(rp, st + C::kR, wave, lane);
-        kp += (uint64_t)krow * kDC;
-        qp += (uint64_t)krow * kDC;
-        vp += (uint64_t)vrow * kDC;
-        rp += d.nheads * R::kBytes;
-    };
+    if (wave == NW) {
+        // the feeding wavefront
+        DTileCopy<C::kCH, 1, WTile<C::kCH>> kcopy;
+        DTileCopy<C::kCV, 1, VTile<C::kCV>> vcopy;
+        kcopy.plan(krow, 0, lane);
+        vcopy.plan(vrow, 0, lane);
+        auto issue = [&](int c) __attribute__((always_inline)) {
+            const unsigned st = lds0 + (unsigned)(c % kBuf) * C::kStage;
+            const int rows = sq.len - c * kDC;
+            const uint64_t tok = (uint64_t)c * kDC;
+            kcopy.issue(reinterpret_cast<const unsigned char*>(kbase) + tok * krow, krow, rows, valid, st + C::kK, 0, lane);
+            kcopy.issue(reinterpret_cast<const unsigned char*>(qbase) + tok * krow, krow, rows, valid, st + C::kQ, 0, lane);
+            vcopy.issue(reinterpret_cast<const unsigned char*>(vbase) + tok * vrow, vrow, rows, C::kCV, st + C::kV, 0, lane);
+#pragma unroll
+            for (int i = 0; i < NH; ++i)
+                linear_copy<R::kFwdBytes, 1>(rbase + ((int64_t)c * d.nheads + i) * R::kBytes, st + C::kR + i * R::kFwdBytes, 0, lane);
+        };
+        for (int c = 0; c < kBuf - 1 && c < nblk; ++c) issue(c);
+        for (int c = 0; c < nblk; ++c) {
+            // Stage c is there when no more than the later stages' copies are outstanding (the counter goes down in
+            // order). The last block may have fewer (rows past the sequence are written, not copied): with it in
+            // flight, everything is waited for.
+            constexpr int kLater = (kBuf - 2) * C::kCopies < 63 ? (kBuf - 2) * C::kCopies : 63;
+            if (c + kBuf - 1 >= nblk) wait_vmem(); else wait_vmem_below<kLater>();
+            __syncthreads();                              // and everybody is done with the stage before it
+            if (c + kBuf - 1 < nblk) issue(c + kBuf - 1);
+        }
+        return;
+    }
 
-    // S^T in accumulator tiles: tile t = 2 kb + x, rows 4g + m = columns ncol(t) + m of the state, column r = its row p
+    // S^T in accumulator tiles: tile t = 2 kb + x, rows 4g + m = columns ncol(t) + m of the state, column r = its row pv + r
     auto ncol = [&](int t) { return 32 * (t >> 1) + 8 * g + 4 * (t & 1); };
+    const int64_t srow = (sh * P + pv + r) * N;
     f32x4 S[2 * NB];
 #pragma unroll
     for (int t = 0; t < 2 * NB; ++t) {
         S[t] = f32x4{0.f, 0.f, 0.f, 0.f};
-        if (init && ncol(t) < N) {
-            const float4 a = *reinterpret_cast<const float4*>(init + (sh * P + p) * N + ncol(t));
-            S[t] = f32x4{a.x, a.y, a.z, a.w};
-        }
+        if (init && ncol(t) < N) S[t] = *reinterpret_cast<const f32x4*>(init + srow + ncol(t));
     }
-    wait_vmem();          // so that no register load is in flight among the copies that are counted below
-#pragma unroll
-    for (int c = 0; c < kBuf - 1; ++c)
-        if (c < nblk) issue(c, c);
-
+    auto pair_of = [&](Pair<T>& f, const f32x4& a, const f32x4& b) __attribute__((always_inline)) {
+        const float sv[8] = {a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+        f.set(sv);
+    };
     // the state entering a chunk of 64 tokens (k = 0 ..) and after the last one
     auto keep_state = [&](int k) __attribute__((always_inline)) {
-        const int64_t at = keep.state_at(((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h, pw / 16 + wave, lane, d);
+        const int64_t at = keep.state_at(((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h, pv / 16, lane, d);
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
             if (32 * kb < N) {
-                const float sv[8] = {S[2 * kb][0], S[2 * kb][1], S[2 * kb][2], S[2 * kb][3],
-                                     S[2 * kb + 1][0], S[2 * kb + 1][1], S[2 * kb + 1][2], S[2 * kb + 1][3]};
                 Pair<T> s;
-                s.set(sv);
+                pair_of(s, S[2 * kb], S[2 * kb + 1]);
                 store8(keep.S + at + kb * keep.kb_stride, s.hi);
                 if constexpr (sizeof(T) == 2) store8(keep.Slo + at + kb * keep.kb_stride, s.lo);
             }
         }
     };
-
     // dy of this lane's tokens and 4 columns in the columns = tokens form, fetched a block ahead
     f32x4 dyv[2], dyn[2];
-    auto fetch_dy = [&](f32x4 (&o)[2], int c) __attribute__((always_inline)) {
+    auto fetch_dy = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int64_t tok = sq.start + min(c * kDC + perm32(t, r), sq.len - 1);
-            const float4 f = load4f(keep.dy + (tok * d.nheads + h) * P + pw + 16 * wave + 4 * g);
-            o[t] = f32x4{f.x, f.y, f.z, f.w};
+            const float4 f = load4f(keep.dy + (tok * d.nheads + h) * P + pv + 4 * g);
+            dyn[t] = f32x4{f.x, f.y, f.z, f.w};
         }
     };
     // block c in stage b (a constant: the loop is unrolled over the ring)
     auto step = [&](int c, auto stage) __attribute__((always_inline)) {
         constexpr int b = decltype(stage)::value;
-        // This stage's copies are done when what was started after them is all that is outstanding (the counter goes
-        // down in order): the later stages' copies and the last block's kStores stores.
-        constexpr int kStores = kBwd ? 3 : 2;
-        constexpr int kLater = (kBuf - 2) * C::kMin < 63 - kStores ? (kBuf - 2) * C::kMin : 63 - kStores;
-        if (c + kBuf - 2 >= nblk) wait_vmem();
-        else if (c > 0) wait_vmem_below<kLater + kStores>();
-        else wait_vmem_below<kLater>();
-        __syncthreads();                                  // and everybody is done with the stage before it
+        __syncthreads();                                  // the stage is filled
         if constexpr (kBwd) {
             if (c % 2 == 0) keep_state(c / 2);
 #pragma unroll
             for (int t = 0; t < 2; ++t) dyv[t] = dyn[t];
-            if (c + 1 < nblk) fetch_dy(dyn, c + 1);
+            if (c + 1 < nblk) fetch_dy(c + 1);
         }
-        if (c + kBuf - 1 < nblk) issue(c + kBuf - 1, (b + kBuf - 1) % kBuf);
-        const unsigned st = lds0 + b * C::kStage, rec = st + C::kR, tab = rec + R::kTab;
+        const unsigned st = lds0 + b * C::kStage, rec = st + C::kR + hw * R::kFwdBytes, tab = rec + R::kTab;
         const int rows = min(kDC, sq.len - c * kDC);
 
         // what does not depend on the state first
@@ -186,31 +188,31 @@ __device__ __forceinline__ void chain(
             gt[t] = lds_at<float>(tab + 4 * perm32(t, r));
         }
 
+        // K S^T (rows tokens, columns p) and S Q^T (rows p, columns tokens)
         f32x4 ks[2], yt[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) ks[t] = yt[t] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
-            Pair<T> s;
-            const float sv[8] = {S[2 * kb][0], S[2 * kb][1], S[2 * kb][2], S[2 * kb][3],
-                                 S[2 * kb + 1][0], S[2 * kb + 1][1], S[2 * kb + 1][2], S[2 * kb + 1][3]};
-            s.set(sv);
+            Pair<T> p;
+            pair_of(p, S[2 * kb], S[2 * kb + 1]);
+            S[2 * kb] *= gl;
+            S[2 * kb + 1] *= gl;
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 Vec8<T> kf, qf;
                 krows.load(kf, st + C::kK, t, kb);
-                mma_xp(ks[t], kf, s);
+                mma_xp(ks[t], kf, p);
                 krows.load(qf, st + C::kQ, t, kb);
-                if constexpr (kBwd) mma_px(yt[t], s, qf); else mma(yt[t], s.hi, qf);
+                if constexpr (kBwd) mma_px(yt[t], p, qf); else mma(yt[t], p.hi, qf);
             }
         }
         // E = V - gam K S^T (zero in rows past the sequence: their V and K are)
-        float E[8];
+        float E[8], e8[8], dU[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) E[i] = vf.get(i) - gam8[i] * ks[i >> 2][i & 3];
-        Pair<T> ep;
+        Pair<T> ep, du;
         ep.set(E);
-        float e8[8], dU[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
@@ -224,7 +226,7 @@ __device__ __forceinline__ void chain(
                 f32x4 et = {0.f, 0.f, 0.f, 0.f};
                 mma_pp(et, ep, am[t]);
                 mma_px(et, ep, one);
-                store4(keep.e + keep.frag(sq.slot + c, h, pw / 16 + wave, d) + keep.lane(perm32(t, r), g), et[0], et[1], et[2], et[3]);
+                store4(keep.e + keep.frag(sq.slot + c, h, pv / 16, d) + keep.lane(perm32(t, r), g), et[0], et[1], et[2], et[3]);
             }
         }
         // U = beta e (the forward's records have beta in M and in del)
@@ -236,7 +238,6 @@ __device__ __forceinline__ void chain(
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) dU[i] = e8[i] * del8[i];
-        Pair<T> du;
         du.set(dU);
 #pragma unroll
         for (int t = 0; t < 2; ++t) yt[t] *= gt[t];
@@ -250,14 +251,15 @@ __device__ __forceinline__ void chain(
                 dot[t] = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
             }
             // (32 tokens as 2 x 64 bytes, each twice; what is past the sequence is not read)
-            keep.ydy[(((pw / 16 + wave) * d.seqs + sh / d.nheads) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
+            keep.ydy[((pv / 16 * d.seqs + sh / d.nheads) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
                 sum_groups(dot[0], dot[1]);
         } else {
             Vec8<T> uf;
             pack8(uf, e8);
+            // rows past the sequence are outside the buffer: dropped
             const auto out = __builtin_amdgcn_make_buffer_rsrc(
-                y + ((sq.start + c * kDC) * d.nheads + h) * P + pw + 16 * wave, 0, (rows - 1) * (int)vrow + 16 * (int)sizeof(T),
-                kBufferDword3);
+                y + ((sq.start + c * kDC) * d.nheads + h) * P + pv, 0,
+                (rows - 1) * (int)vrow + 16 * (int)sizeof(T), kBufferDword3);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 mma(yt[t], uf, mm[t].hi);
@@ -266,14 +268,13 @@ __device__ __forceinline__ void chain(
         }
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
-            S[t] *= gl;
             Vec8<T> kf;
             kcols.load(kf, st + C::kK, t & 1, t >> 1);
             mma_xp(S[t], kf, du);
         }
     };
     if constexpr (kBwd) {
-        if (nblk > 0) fetch_dy(dyn, 0);
+        if (nblk > 0) fetch_dy(0);
     }
     for (int c = 0; c < nblk; c += kBuf) {
         step(c, std::integral_constant<int, 0>());
@@ -287,7 +288,7 @@ __device__ __forceinline__ void chain(
     } else {
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t)
-            if (ncol(t) < N) store4(fin + (sh * P + p) * N + ncol(t), S[t][0], S[t][1], S[t][2], S[t][3]);
+            if (ncol(t) < N) *reinterpret_cast<f32x4*>(fin + srow + ncol(t)) = S[t];
     }
 }
 
@@ -295,35 +296,35 @@ __device__ __forceinline__ void chain(
 // takes two moves: the bf16 kernels are held to two wavefronts per SIMD, and their LDS is sized at the launch, so
 // that the compiler does not conclude from it that there is but one. The fp32 ones, whose fragments take
 // twice the registers, need the others.
-template <typename T, int NB, int NW, bool kBwd>
-__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void delta_chain_kernel(
+template <typename T, int NB, int NW, int NH, bool kBwd>
+__global__ __launch_bounds__(64 * (NW + 1)) __attribute__((amdgpu_waves_per_eu(NW > 4 ? 3 : 2, NW > 4 ? 3 : 2))) void delta_chain_kernel(
     const T* v, const T* Km, const T* Qm, const float* init, const unsigned char* recs, T* y, float* fin,
     DeltaKeep<T> keep, DeltaDims d, int nslice)
 {
-    chain<T, NB, NW, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
+    chain<T, NB, NW, NH, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
 }
-template <typename T, int NB, int NW, bool kBwd>
-__global__ __launch_bounds__(64 * NW) void delta_chain_f32_kernel(
+template <typename T, int NB, int NW, int NH, bool kBwd>
+__global__ __launch_bounds__(64 * (NW + 1)) void delta_chain_f32_kernel(
     const T* v, const T* Km, const T* Qm, const float* init, const unsigned char* recs, T* y, float* fin,
     DeltaKeep<T> keep, DeltaDims d, int nslice)
 {
-    chain<T, NB, NW, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
+    chain<T, NB, NW, NH, kBwd>(v, Km, Qm, init, recs, y, fin, keep, d, nslice);
 }
 
-template <typename T, int NB, int NW, bool kBwd>
+template <typename T, int NB, int NW, int NH, bool kBwd>
 hipError_t launch_chain(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
                         float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream)
 {
-    const int nslice = (int)d.headdim / (16 * NW);
-    const int64_t nblocks = d.seqs * d.nheads * nslice;
+    const int nslice = (int)d.headdim * NH / (16 * NW);
+    const int64_t nblocks = d.seqs * (d.nheads / NH) * nslice;
     if (nblocks == 0) return hipSuccess;
-    using C = ChainCfg<T, NB, NW, kBwd>;
-    constexpr unsigned kLds = C::kBuf * C::kStage;
+    using C = ChainCfg<T, NB, NW, NH, kBwd>;
+    constexpr unsigned kLds = C::kLds;
     if constexpr (sizeof(T) == 2)
-        hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), kLds,
+        hipLaunchKernelGGL((delta_chain_kernel<T, NB, NW, NH, kBwd>), dim3((unsigned)nblocks), dim3(64 * (NW + 1)), kLds,
                            stream, v, k, q, init, rec, y, fin, keep, d, nslice);
     else
-        hipLaunchKernelGGL((delta_chain_f32_kernel<T, NB, NW, kBwd>), dim3((unsigned)nblocks), dim3(64 * NW), kLds,
+        hipLaunchKernelGGL((delta_chain_f32_kernel<T, NB, NW, NH, kBwd>), dim3((unsigned)nblocks), dim3(64 * (NW + 1)), kLds,
                            stream, v, k, q, init, rec, y, fin, keep, d, nslice);
     return hipGetLastError();
 }
@@ -332,11 +333,24 @@ template <typename T, int NB, bool kBwd>
 hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, const unsigned char* rec, T* y,
                      float* fin, const DeltaKeep<T>& keep, const DeltaDims& d, hipStream_t stream)
 {
-    if (d.headdim == 16) return launch_chain<T, NB, 1, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+#define SSD_CHAIN(NW, NH) return launch_chain<T, NB, NW, NH, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream)
+    if constexpr (sizeof(T) == 2 && NB <= 4) {
+        // More workgroups of 64 columns than CUs, and a second one does not fit a CU beside the first (its five
+        // wavefronts would put four on one SIMD): eight wavefronts that share K and Q, two heads of 64 columns or one
+        // of 128. 320 heads of 64 x 128 over 4096 tokens: 226 us against 273. With fewer, four: 192 heads over 2048
+        // tokens take 74 us. Sequences of different lengths keep to four, which are faster one by one: a batch whose
+        // longest sequence holds 4096 of 16384 tokens takes 325 us, with eight 360.
+        constexpr int64_t kCUs = 256;
+        if (!d.cu && d.seqs * d.nheads * d.headdim > 64 * kCUs) {
+            if (d.headdim == 128) SSD_CHAIN(8, 1);
+            if (d.headdim == 64 && d.nheads / d.ngroups % 2 == 0) SSD_CHAIN(8, 2);
+        }
+    }
+    if (d.headdim == 16) SSD_CHAIN(1, 1);
     // two stages of the widest fp32 rows leave room for two wavefronts' columns
-    if (d.headdim == 32 || sizeof(T) * NB == 32)
-        return launch_chain<T, NB, 2, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
-    if constexpr (sizeof(T) * NB < 32) return launch_chain<T, NB, 4, kBwd>(v, k, q, init, rec, y, fin, keep, d, stream);
+    if (d.headdim == 32 || sizeof(T) * NB == 32) SSD_CHAIN(2, 1);
+    if constexpr (sizeof(T) * NB < 32) SSD_CHAIN(4, 1);
+#undef SSD_CHAIN
     return hipErrorInvalidValue;
 }
 

@@ -113,6 +113,7 @@ __device__ __forceinline__ void unit_lower_inverse(float* lt, unsigned char* m0,
         for (int q = 0; q < 4; ++q) w = __builtin_amdgcn_mfma_f32_16x16x4f32(l21[q], a2[q], w, 0, 0, 0);
 #pragma unroll
         for (int q = 0; q < 4; ++q) x = __builtin_amdgcn_mfma_f32_16x16x4f32(t[(4 * g + q) * kLd + r], w[q], x, 0, 0, 0);
+        settle();
         const float v[4] = {-x[0], -x[1], -x[2], -x[3]};
         unsigned char* const me = e ? m1 : m0;
         if (me) put4<true>(me, 16 + r, 4 * g, v, T());

@@ -153,7 +153,7 @@ struct VTile {
 template <int CH, int NW, class TL = DTile<CH>>
 struct DTileCopy {
     static constexpr int kI = DTile<CH>::kInst, kK = (kI + NW - 1) / NW;
-    static constexpr bool kPlan = kK <= 8;        // more offsets would crowd the registers: worked out each time
+    static constexpr bool kPlan = kK <= 16;       // more offsets would crowd the registers: worked out each time
     unsigned off[kPlan ? kK : 1];
     __device__ __forceinline__ static void place(int q, int lane, int& r, int& c)
     {
@@ -373,6 +373,16 @@ template <> struct Pair<float> {
     Vec8<float> hi;
     __device__ __forceinline__ void set(const float (&v)[8]) { pack8(hi, v); }
 };
+// Between matrix instructions and a branch behind which their results are read: the compiler's count of the wait states
+// that they need was seen to fall short across the branch (a conversion read two of four result registers too
+// early), so the longest wait is spent before it.
+__device__ __forceinline__ void settle()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // a exact, b a pair and the other way round; both pairs: without the product of the two low parts (2^-18)
 __device__ __forceinline__ void mma_px(f32x4& acc, const Pair<bf16>& a, const Vec8<bf16>& b) { mma(acc, a.lo, b); mma(acc, a.hi, b); }
 __device__ __forceinline__ void mma_px(f32x4& acc, const Pair<float>& a, const Vec8<float>& b) { mma(acc, a.hi, b); }
