@@ -285,8 +285,9 @@ __device__ __forceinline__ void walk_back(
             Vec8<T> one;
             unit_frag(one, t, r, g);
             f32x4 w = du[t], wt = {0.f, 0.f, 0.f, 0.f};
-            mma_pp(w, bm[t], dup);
-            mma_pp(wt, dup, bm[t]);
+            mma_pp<true>(w, bm[t], dup);
+            mma_pp<true>(wt, dup, bm[t]);
+            mma_rest(wt, dup, dU, one);
             mma_px(wt, dup, one);
 #pragma unroll
             for (int m = 0; m < 4; ++m) bw[4 * t + m] = -ga[4 * t + m] * bt8[4 * t + m] * w[m];

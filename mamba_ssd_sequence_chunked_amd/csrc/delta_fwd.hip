@@ -10,10 +10,14 @@
 //   S^T = gam_last S^T + K^T (diag(del) U)
 //
 // For bf16 inputs S, A, E and del U are pairs of bf16 values where they lead to the state (fp32 to about 2^-17);
-// where they lead to y only, which is rounded to bf16 itself, S and U are rounded to bf16 once.
+// where they lead to y only, which is rounded to bf16 itself, S and M are rounded to bf16 once: y is off by 2.4e-3 in
+// the 2-norm, of which its own rounding is 1.7e-3. (U is a pair there too, at 2 more matrix instructions a block: 2.8e-3
+// without. S as one would cost 8 and 6 % of the time, for 0.1e-3.)
 //
 // kBwd is the backward's walk forward: the same block by block, with y kept to fp32's accuracy (pairs there too)
-// and, in place of y and the final state, what the walk back and the gradients of k and q need (DeltaKeep).
+// and, in place of y and the final state, what the walk back and the gradients of k and q need (DeltaKeep). dg is
+// the small difference of dy . y and dv . v, so what these are made of is carried further: the low parts' product and
+// the third bf16 piece of E and U take its error from 7e-6 to 4.6e-6, with decays down to e^-40 from 2.8e-5 to 7e-6.
 //
 // A workgroup = NW wavefronts that walk (16 rows each, of one head or of NH next to each other) and one that feeds
 // them: K, Q, the V columns and the blocks' records come through a ring of kBuf stages of asynchronous global -> LDS
@@ -216,7 +220,7 @@ __device__ __forceinline__ void chain(
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
-            mma_pp(e, am[t], ep);
+            mma_pp<kBwd>(e, am[t], ep);
 #pragma unroll
             for (int m = 0; m < 4; ++m) e8[4 * t + m] = e[m];
             if constexpr (kBwd) {
@@ -224,7 +228,8 @@ __device__ __forceinline__ void chain(
                 Vec8<T> one;
                 unit_frag(one, t, r, g);
                 f32x4 et = {0.f, 0.f, 0.f, 0.f};
-                mma_pp(et, ep, am[t]);
+                mma_pp<true>(et, ep, am[t]);
+                mma_rest(et, ep, E, one);
                 mma_px(et, ep, one);
                 store4(keep.e + keep.frag(sq.slot + c, h, pv / 16, d) + keep.lane(perm32(t, r), g), et[0], et[1], et[2], et[3]);
             }
@@ -247,22 +252,23 @@ __device__ __forceinline__ void chain(
             float dot[2];
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                mma_pp(yt[t], up, mm[t]);
+                mma_rest(yt[t], up, e8, mm[t].hi);
+                mma_pp<true>(yt[t], up, mm[t]);
                 dot[t] = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
             }
             // (32 tokens as 2 x 64 bytes, each twice; what is past the sequence is not read)
             keep.ydy[((pv / 16 * d.seqs + sh / d.nheads) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
                 sum_groups(dot[0], dot[1]);
         } else {
-            Vec8<T> uf;
-            pack8(uf, e8);
+            Pair<T> up;
+            up.set(e8);
             // rows past the sequence are outside the buffer: dropped
             const auto out = __builtin_amdgcn_make_buffer_rsrc(
                 y + ((sq.start + c * kDC) * d.nheads + h) * P + pv, 0,
                 (rows - 1) * (int)vrow + 16 * (int)sizeof(T), kBufferDword3);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
-                mma(yt[t], uf, mm[t].hi);
+                mma_px(yt[t], up, mm[t].hi);
                 buffer_store4(out, perm32(t, r) * (int)vrow + 4 * g * (int)sizeof(T), 0, yt[t], T());
             }
         }
@@ -338,7 +344,7 @@ hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, cons
         // More workgroups of 64 columns than CUs, and a second one does not fit a CU beside the first (its five
         // wavefronts would put four on one SIMD): eight wavefronts that share K and Q, two heads of 64 columns or one
         // of 128. 320 heads of 64 x 128 over 4096 tokens: 226 us against 273. With fewer, four: 192 heads over 2048
-        // tokens take 74 us. Sequences of different lengths keep to four, which are faster one by one: a batch whose
+        // tokens take 75 us. Sequences of different lengths keep to four, which are faster one by one: a batch whose
         // longest sequence holds 4096 of 16384 tokens takes 325 us, with eight 360.
         constexpr int64_t kCUs = 256;
         if (!d.cu && d.seqs * d.nheads * d.headdim > 64 * kCUs) {

@@ -383,18 +383,32 @@ __device__ __forceinline__ void settle()
     __builtin_amdgcn_sched_barrier(0);
 }
 
-// a exact, b a pair and the other way round; both pairs: without the product of the two low parts (2^-18)
+// a exact, b a pair and the other way round; both pairs: without the product of the two low parts (2^-18), or with it
 __device__ __forceinline__ void mma_px(f32x4& acc, const Pair<bf16>& a, const Vec8<bf16>& b) { mma(acc, a.lo, b); mma(acc, a.hi, b); }
 __device__ __forceinline__ void mma_px(f32x4& acc, const Pair<float>& a, const Vec8<float>& b) { mma(acc, a.hi, b); }
 __device__ __forceinline__ void mma_xp(f32x4& acc, const Vec8<bf16>& a, const Pair<bf16>& b) { mma(acc, a, b.lo); mma(acc, a, b.hi); }
 __device__ __forceinline__ void mma_xp(f32x4& acc, const Vec8<float>& a, const Pair<float>& b) { mma(acc, a, b.hi); }
+template <bool kLow = false>
 __device__ __forceinline__ void mma_pp(f32x4& acc, const Pair<bf16>& a, const Pair<bf16>& b)
 {
+    if constexpr (kLow) mma(acc, a.lo, b.lo);
     mma(acc, a.lo, b.hi);
     mma(acc, a.hi, b.lo);
     mma(acc, a.hi, b.hi);
 }
+template <bool kLow = false>
 __device__ __forceinline__ void mma_pp(f32x4& acc, const Pair<float>& a, const Pair<float>& b) { mma(acc, a.hi, b.hi); }
+// The product of b with what the pair a of v leaves of it.
+__device__ __forceinline__ void mma_rest(f32x4& acc, const Pair<bf16>& a, const float (&v)[8], const Vec8<bf16>& b)
+{
+    float left[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) left[i] = v[i] - a.hi.get(i) - a.lo.get(i);
+    Vec8<bf16> f;
+    pack8(f, left);
+    mma(acc, f, b);
+}
+__device__ __forceinline__ void mma_rest(f32x4&, const Pair<float>&, const float (&)[8], const Vec8<float>&) {}
 
 // The matrices of a record (tiles of kRecCH chunks a row): pairs by rows and by columns (tile x).
 template <typename T> constexpr int kRecCH = 32 * (int)sizeof(T) / 16;
