@@ -315,7 +315,7 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *     every g below -1000 acts as -1000 (exp is 0 in fp32 from -104 on), so -inf is a reset.
  *   - k is used as given.  The recurrence is stable for beta |k|^2 < 2: callers scale k to at most unit
  *     length.  q carries any scale the caller wants on y.
- *   - 0 <= batch <= 65535; nseq <= 2^24; (tokens / 32 + rows) * nheads < 2^24 and rows * nheads * headdim < 2^30,
+ *   - 0 <= batch <= 65535; nseq <= 2^24; (tokens / 32 + rows) * nheads < 2^24 and rows * nheads * headdim < 2^29,
  *     rows being batch or nseq (for ssd_delta_step batch * nheads < 2^24).  There is no chunk size.
  *   - With bf16 inputs the final states and the fp32 gradients keep fp32's accuracy (about 1e-5 of their
  *     norm): every fp32 operand of a matrix-core product that reaches them is carried as a pair of bf16

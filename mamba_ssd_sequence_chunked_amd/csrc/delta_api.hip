@@ -15,10 +15,10 @@ int check_delta(const DeltaDims& d)
     if (rc != SSD_OK) return rc;
     if (d.seqs < 0 || d.seqs > (int64_t(1) << 24) || d.seqlen < 0 || d.tokens < 0) return SSD_ERR_SHAPE;
     if (d.tokens > INT32_MAX) return SSD_ERR_SHAPE;                      // cu_seqlens holds 32-bit offsets
-    // one-dimensional grids of fewer than 2^32 threads: 256 a (block of 32 tokens, head), 64 a (row, head, 16 of
-    // the head dimension)
+    // one-dimensional grids of fewer than 2^32 threads: 256 a (block of 32 tokens, head); a (row, head) 128 to 192 for
+    // each 16 or 32 columns of v, which the first limit covers, or 80 for each 16, for which there is the second
     if ((d.tokens / 32 + d.seqs) * d.nheads >= (int64_t(1) << 24)) return SSD_ERR_SHAPE;
-    if (d.seqs * d.nheads * d.headdim >= (int64_t(1) << 30)) return SSD_ERR_SHAPE;
+    if (d.seqs * d.nheads * d.headdim >= (int64_t(1) << 29)) return SSD_ERR_SHAPE;
     if (d.tokens * d.nheads * (d.headdim > d.dstate ? d.headdim : d.dstate) > (int64_t(1) << 40)) return SSD_ERR_SHAPE;
     if (d.seqs * d.nheads * d.headdim * d.dstate > (int64_t(1) << 40)) return SSD_ERR_SHAPE;
     return SSD_OK;

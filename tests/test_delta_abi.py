@@ -36,6 +36,7 @@ def forward(**kw):
     (dict(b=2, L=1 << 30), ERR_SHAPE),                    # 2^31 tokens
     (dict(b=1, L=1 << 27), ERR_SHAPE),                    # 2^24 blocks of 32 tokens x heads
     (dict(b=60000, L=(1 << 62)), ERR_SHAPE),              # the product would overflow
+    (dict(b=65535, L=1, H=129, P=64), ERR_SHAPE),         # 2^29 rows x heads x columns of v
     (dict(v=None), ERR_NULL), (dict(g=None), ERR_NULL), (dict(fin=None), ERR_NULL), (dict(ws=None), ERR_NULL),
     (dict(ws_bytes=8), ERR_WS),
     (dict(y=fake(1)), ERR_ALIAS), (dict(fin=fake(6)), ERR_ALIAS), (dict(init=fake(7)), ERR_ALIAS),
