@@ -61,16 +61,19 @@ __device__ __forceinline__ void chain(
     static_assert(C::kLds <= 160 * 1024, "ring");
     extern __shared__ __attribute__((aligned(1024))) unsigned char ring[];        // C::kLds
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-    const int bid = xcd_logical_block(blockIdx.x, gridDim.x);
+    // An XCD takes neighbouring heads, which share K and Q; but sequences of different lengths are dealt out, so that no
+    // XCD is left with the long ones (7 of 64 to 4096 tokens, 80 heads: 244 us against 319; started from the longest
+    // 223, but ranking them costs 37 short ones 56 us against 46).
+    const int bid = d.cu ? (int)blockIdx.x : xcd_logical_block(blockIdx.x, gridDim.x);
     const int slice = bid % nslice;
-    const int64_t sh0 = bid / nslice * NH;
-    const int h0 = (int)(sh0 % d.nheads);                 // the workgroup's (first) head
-    const DeltaSeq sq = delta_seq(d, sh0 / d.nheads);
+    const int h0 = (int)(bid / nslice * (int64_t)NH % d.nheads);       // the workgroup's (first) head
+    const int64_t s = bid / nslice * (int64_t)NH / d.nheads;
+    const DeltaSeq sq = delta_seq(d, s);
     const int grp = h0 / (int)(d.nheads / d.ngroups);
     const int N = (int)d.dstate, P = (int)d.headdim;
     const int pw = 16 * (NW / NH) * slice;                // the workgroup's first column of v
     const int hw = wave / (NW / NH), h = h0 + hw;         // this wavefront's head
-    const int64_t sh = sh0 + hw;
+    const int64_t sh = s * d.nheads + h;
     const int pv = pw + 16 * (wave % (NW / NH));          // and first column
     const int nblk = (sq.len + kDC - 1) / kDC;
     const int valid = N * (int)sizeof(T) / 16;
@@ -143,7 +146,7 @@ __device__ __forceinline__ void chain(
     };
     // the state entering a chunk of 64 tokens (k = 0 ..) and after the last one
     auto keep_state = [&](int k) __attribute__((always_inline)) {
-        const int64_t at = keep.state_at(((sh / d.nheads) * (keep.chunks + 1) + k) * d.nheads + h, pv / 16, lane, d);
+        const int64_t at = keep.state_at((s * (keep.chunks + 1) + k) * d.nheads + h, pv / 16, lane, d);
 #pragma unroll
         for (int kb = 0; kb < NB; ++kb) {
             if (32 * kb < N) {
@@ -257,7 +260,7 @@ __device__ __forceinline__ void chain(
                 dot[t] = yt[t][0] * dyv[t][0] + yt[t][1] * dyv[t][1] + yt[t][2] * dyv[t][2] + yt[t][3] * dyv[t][3];
             }
             // (32 tokens as 2 x 64 bytes, each twice; what is past the sequence is not read)
-            keep.ydy[((pv / 16 * d.seqs + sh / d.nheads) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
+            keep.ydy[((pv / 16 * d.seqs + s) * d.nheads + h) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
                 sum_groups(dot[0], dot[1]);
         } else {
             Pair<T> up;
@@ -343,11 +346,11 @@ hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, cons
     if constexpr (sizeof(T) == 2 && NB <= 4) {
         // More workgroups of 64 columns than CUs, and a second one does not fit a CU beside the first (its five
         // wavefronts would put four on one SIMD): eight wavefronts that share K and Q, two heads of 64 columns or one
-        // of 128. 320 heads of 64 x 128 over 4096 tokens: 226 us against 273. With fewer, four: 192 heads over 2048
-        // tokens take 75 us. Sequences of different lengths keep to four, which are faster one by one: a batch whose
-        // longest sequence holds 4096 of 16384 tokens takes 325 us, with eight 360.
+        // of 128. 320 heads of 64 x 128 over 4096 tokens: 226 us against 273; 7 sequences of 64 to 4096 tokens, 80
+        // heads: 224 against 249; 37 of 1 to 150, 16 heads of 128 x 128: 40 against 46. With fewer, four: 192 heads over
+        // 2048 tokens take 75 us.
         constexpr int64_t kCUs = 256;
-        if (!d.cu && d.seqs * d.nheads * d.headdim > 64 * kCUs) {
+        if (d.seqs * d.nheads * d.headdim > 64 * kCUs) {
             if (d.headdim == 128) SSD_CHAIN(8, 1);
             if (d.headdim == 64 && d.nheads / d.ngroups % 2 == 0) SSD_CHAIN(8, 2);
         }
