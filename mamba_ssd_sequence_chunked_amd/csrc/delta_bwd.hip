@@ -317,6 +317,7 @@ __device__ __forceinline__ void walk_back(
             kcols.load(kf, st + C::kK, t & 1, t >> 1);
             mma_xp(H[t], kf, bwp);
         }
+        settle();                                         // H is read behind the loop's branches
     };
     for (int c = nblk - 1; c >= 0; c -= 2) {
         step(c, std::integral_constant<int, 0>());

@@ -281,6 +281,7 @@ __device__ __forceinline__ void chain(
             kcols.load(kf, st + C::kK, t & 1, t >> 1);
             mma_xp(S[t], kf, du);
         }
+        settle();                                         // S is read behind the loop's branches
     };
     if constexpr (kBwd) {
         if (nblk > 0) fetch_dy(0);
