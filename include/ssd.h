@@ -318,8 +318,8 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *   - 0 <= batch <= 65535; nseq <= 2^24; (tokens / 32 + rows) * nheads < 2^24 and rows * nheads * headdim < 2^29,
  *     rows being batch or nseq (for ssd_delta_step batch * nheads < 2^24).  There is no chunk size.
  *   - With bf16 inputs the final states and the fp32 gradients keep fp32's accuracy (about 1e-5 of their
- *     norm): every fp32 operand of a matrix-core product that reaches them is carried as a pair of bf16
- *     values.
+ *     norm, twice that where all keys of a row are alike): every fp32 operand of a matrix-core product
+ *     that reaches them is carried as a pair of bf16 values.
  *   - Non-finite inputs: the sums run over blocks of 32 tokens in which a later token's values carry a
  *     weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of the same
  *     32-token block of its sequence (and all later ones), never another sequence, batch row or group.

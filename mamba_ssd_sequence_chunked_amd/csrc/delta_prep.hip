@@ -11,6 +11,10 @@
 // wavefront), the corner by eight fp32 matrix instructions.  (Not by powers of L: for a block of like keys their
 // entries grow to binomials and cancel.)  The log decays are summed and subtracted in 64 bits, so that a strong
 // decay early in a block costs later pairs no digits.
+//
+// Bound by the records' bytes and by the substitutions' chain of 16 dependent rows: 4 x 4096 tokens, 80 heads
+// (bf16, N = 128) 85 us for 273 MB of records, 140 us for the backward's 524 MB. Forward substitution of whole 32 x 32
+// matrices took 140 us and 370.
 #include "delta_tiles.hpp"
 
 namespace ssd {

@@ -8,6 +8,7 @@ there is no fallback: without the built library every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional, Tuple
@@ -117,7 +118,7 @@ def _need(t: Optional[torch.Tensor], name: str, shape, dtype, device) -> None:
         raise ValueError(f"{name} is required")
     if not isinstance(t, torch.Tensor):
         raise ValueError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -372,7 +373,7 @@ def selective_scan(x: torch.Tensor, delta: torch.Tensor, A: torch.Tensor, B: tor
 
 def _on_device(device):
     """The device the tensors are on made current for the launch, if it is not."""
-    return torch.cuda.device(device)
+    return contextlib.nullcontext() if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
 def _delta_need(v, g, beta, k, q, lead, H, P, N, G, dev):
