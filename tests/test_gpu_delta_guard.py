@@ -149,3 +149,68 @@ def test_many_heads_backward():
         assert rel2(f64(got[n]), want[n]) <= 4 * state_unit("bf16", 48), n
     for n in ("dv", "dk", "dq"):
         assert rel2(f64(got[n]), want[n]) <= 4 * ROUND["bf16"], n
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 elements of v: the sequence in two parts, cut at a chunk's end, gives the same bits.
+
+    Not so the second part's dbeta and dg: the state it starts from is the forward's, which sums three of the four
+    products of two pairs, while the whole backward goes on from its own walk's, which sums all four. Each is within
+    four of the state's units of the exact gradient (as in test_gpu_delta.test_backward), so they are within eight of
+    each other; an offset that wrapped would be off by their whole size."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    H, P, N, L, cut = 128, 128, 16, (1 << 18) + 197, 1 << 17
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    bf = lambda *s: torch.empty(1, L, *s, dtype=torch.bfloat16, device="cuda").normal_(generator=gen)   # noqa: E731
+    v, dy, k, q = bf(H, P), bf(H, P), bf(1, N), bf(1, N)
+    assert v.numel() > 1 << 32
+    k = torch.nn.functional.normalize(k.float(), dim=-1).bfloat16()
+    q = torch.nn.functional.normalize(q.float(), dim=-1).bfloat16()
+    g = -0.1 * torch.rand(1, L, H, device="cuda", generator=gen)
+    beta = torch.rand(1, L, H, device="cuda", generator=gen)
+    x = (v, g, beta, k, q)
+    a, z = [t[:, :cut] for t in x], [t[:, cut:] for t in x]
+
+    y, fin = ssd.delta_forward(*x)
+    ya, mid = ssd.delta_forward(*a)
+    yz, end = ssd.delta_forward(*z, mid)
+    assert torch.isfinite(fin).all() and torch.equal(fin, end)
+    assert torch.equal(y[:, :cut], ya) and torch.equal(y[:, cut:], yz)
+    del y, ya, yz
+
+    whole = ssd.delta_backward(*x, dy)
+    back = ssd.delta_backward(*z, dy[:, cut:], mid)
+    assert torch.equal(whole["dv"][:, cut:], back["dv"])
+    for n in ("dbeta", "dg"):
+        assert (whole[n][:, cut:] - back[n]).norm() <= 8 * state_unit("bf16", N) * back[n].norm(), n
+    front = ssd.delta_backward(*a, dy[:, :cut], None, back["dinit"])
+    assert torch.equal(whole["dinit"], front["dinit"])
+    for n in ("dv", "dbeta", "dg"):
+        assert torch.equal(whole[n][:, :cut], front[n]), n
+    for n in ("dk", "dq"):               # summed over other slices of the heads: fp32 sums, rounded to bf16
+        for w, p in ((whole[n][:, cut:], back[n]), (whole[n][:, :cut], front[n])):
+            assert (w.float() - p.float()).norm() <= 2 * ROUND["bf16"] * p.float().norm(), n
+
+
+def test_two_streams_at_once():
+    """Calls that overlap in time, each on its own workspace."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = [ref.make(2, 700, 6, 64, 128, 2, "bf16", True, seed=50 + i) for i in range(2)]
+    x = [inputs(e) for e in d]
+    h = [dev(e["init"]) for e in d]
+    dy = [dev(e["dy"], "bf16") for e in d]
+    want = [(ssd.delta_forward(*x[i], h[i]), ssd.delta_backward(*x[i], dy[i], h[i])) for i in range(2)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append((ssd.delta_forward(*x[i], h[i]), ssd.delta_backward(*x[i], dy[i], h[i])))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for (y, f), b in got[i]:
+            assert torch.equal(y, want[i][0][0]) and torch.equal(f, want[i][0][1])
+            assert all(torch.equal(b[n], want[i][1][n]) for n in b)
