@@ -257,11 +257,13 @@ constexpr int swz_row_shift(int ch) { return ch >= 16 ? 0 : ch == 8 ? 1 : ch == 
 // possibly aliasing the in-flight copy (it cannot tell the two stage buffers
 // apart and would wait for the prefetch before any LDS read); the kernels
 // order these copies explicitly with wait_vmem() and a barrier.  M0 carries
-// the LDS address and is restored right after the issue.
+// the LDS address and is restored right after the issue.  Between a write of
+// M0 and a copy that reads it the hardware needs one wait state; the compiler
+// spends it for its own copies, but does not look into an asm block.
 __device__ __forceinline__ void dma16(const void* gsrc, unsigned lds_base) {
     const unsigned a = __builtin_amdgcn_readfirstlane(lds_base);
     unsigned saved;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off\n\ts_mov_b32 m0, %0"
                  : "=&s"(saved)
                  : "v"(gsrc), "s"(a)
                  : "memory");
@@ -307,7 +309,7 @@ __device__ __forceinline__ void tiles_load_async(unsigned base, int stride, F sr
 __device__ __forceinline__ void dma16_off(const void* sbase, unsigned voff, unsigned lds_base) {
     const unsigned a = __builtin_amdgcn_readfirstlane(lds_base);
     unsigned saved;
-    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
+    asm volatile("s_mov_b32 %0, m0\n\ts_mov_b32 m0, %3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2\n\ts_mov_b32 m0, %0"
                  : "=&s"(saved)
                  : "v"(voff), "s"(sbase), "s"(a)
                  : "memory");

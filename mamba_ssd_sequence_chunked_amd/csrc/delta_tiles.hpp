@@ -101,7 +101,7 @@ template <typename T, bool kBwd> struct DeltaRec {
 __device__ __forceinline__ void dma16_at(const void* sbase, unsigned voff, unsigned lds_base)
 {
     const unsigned a = __builtin_amdgcn_readfirstlane(lds_base);
-    asm volatile("s_mov_b32 m0, %2\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(a) : "memory");
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(a) : "memory");
 }
 
 // ---- LDS tiles ------------------------------------------------------------------------------------------

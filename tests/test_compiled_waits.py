@@ -1,0 +1,99 @@
+"""Waits that the hardware leaves to the program, looked for in the built library's gfx950 code (no GPU).
+
+The kernels copy global memory to LDS by inline assembly, which the compiler's own count of wait states does not
+look into, so the disassembly is read back and every path through it is followed:
+
+ * a copy to LDS takes its address from M0, and one wait state has to lie between a write of M0 and the copy.
+"""
+import os
+import re
+import shutil
+import subprocess
+
+import pytest
+
+from mamba_ssd_sequence_chunked_amd import _build
+
+LLVM = "/opt/rocm/llvm/bin"
+OBJDUMP = os.path.join(LLVM, "llvm-objdump")
+
+pytestmark = pytest.mark.skipif(not os.path.exists(OBJDUMP), reason="needs the ROCm disassembler")
+
+
+def registers(token):
+    """The registers of an operand, as (class, number)."""
+    token = token.strip().lstrip("-").strip("|")
+    m = re.match(r"^([vas])(\d+)$", token)
+    if m:
+        return [(m[1], int(m[2]))]
+    m = re.match(r"^([vas])\[(\d+):(\d+)\]$", token)
+    if m:
+        return [(m[1], i) for i in range(int(m[2]), int(m[3]) + 1)]
+    return [("m0", 0)] if token == "m0" else []
+
+
+class Ins:
+    __slots__ = ("op", "args", "at", "target", "states", "succ")
+
+    def __init__(self, op, args, at, target):
+        self.op, self.args, self.at, self.target = op, [a.split()[0] if a.split() else "" for a in args.split(",")], at, target
+        self.states = int(self.args[0], 0) + 1 if op == "s_nop" else 1      # wait states that pass with it
+        self.succ = ()
+
+    @property
+    def is_copy(self):
+        return "lds_dword" in self.op
+
+    @property
+    def is_memory(self):
+        return self.op.startswith(("global_", "buffer_", "flat_", "scratch_"))
+
+
+def functions(path):
+    """{name: [Ins]} of a code object, with every instruction's possible successors."""
+    text = subprocess.run([OBJDUMP, "-d", "--no-show-raw-insn", path], capture_output=True, text=True, check=True).stdout
+    out, body = {}, None
+    for line in text.splitlines():
+        m = re.match(r"^[0-9a-f]+ <(.+)>:$", line)
+        if m:
+            body = out.setdefault(m[1], [])
+            continue
+        m = re.match(r"^\t(\S+)\s*(.*?)\s*// ([0-9A-F]+):(.*)$", line)
+        if m and body is not None:
+            to = re.search(r"<.+?(?:\+0x([0-9a-f]+))?>", m[4]) if m[1].startswith(("s_cbranch", "s_branch")) else None
+            body.append(Ins(m[1], m[2], int(m[3], 16), int(to[1] or "0", 16) if to else None))
+    for body in out.values():
+        where = {i.at - body[0].at: n for n, i in enumerate(body)}
+        for n, i in enumerate(body):
+            nxt = [n + 1] if n + 1 < len(body) and i.op not in ("s_branch", "s_endpgm", "s_setpc_b64") else []
+            i.succ = tuple(nxt + ([where[i.target]] if i.target in where else []))
+    return out
+
+
+@pytest.fixture(scope="module")
+def code(tmp_path_factory):
+    """All kernels of the library."""
+    if not os.path.exists(_build.LIB_PATH):
+        _build.build()
+    d = tmp_path_factory.mktemp("code")
+    lib = shutil.copy(_build.LIB_PATH, d)
+    subprocess.run([OBJDUMP, "--offloading", lib], cwd=d, capture_output=True, check=True)
+    out = {}
+    for f in sorted(os.listdir(d)):
+        if f.endswith("gfx950"):
+            out.update(functions(os.path.join(d, f)))
+    assert any("delta_chain" in n for n in out) and any("chunk_scan" in n for n in out)
+    return out
+
+
+def test_copies_to_lds_wait_for_their_address(code):
+    seen = 0
+    for name, body in code.items():
+        for n, i in enumerate(body):
+            if not (i.op.startswith("s_") and i.args[0] == "m0"):
+                continue
+            # no copy right behind a write of M0, on any path
+            for k in i.succ:
+                assert not body[k].is_copy, (name, hex(body[k].at))
+        seen += sum(i.is_copy for i in body)
+    assert seen > 1000
