@@ -465,7 +465,7 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
             const unsigned off = (unsigned)(((rr >> 4) * nkc + kc) * 512 + (16 * gc + (rr & 15)) * 8) * (unsigned)sizeof(T) + 16u * part;
             if (c < valid) {
                 if (rr < rows)
-                    dma16_at(m, off, lds + q * 1024u);
+                    dma16_off(m, off, lds + q * 1024u);
                 else
                     *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(lds + q * 1024u + lane * 16u) = u32x4{0, 0, 0, 0};
             }

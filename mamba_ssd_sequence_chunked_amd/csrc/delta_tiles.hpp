@@ -97,13 +97,6 @@ template <typename T, bool kBwd> struct DeltaRec {
     static constexpr int kRevBytes = kBytes - kM;      // what the walk back reads, from kM on
 };
 
-// The copy of dma16_off without keeping M0 (nothing the compiler emits for these kernels reads it).
-__device__ __forceinline__ void dma16_at(const void* sbase, unsigned voff, unsigned lds_base)
-{
-    const unsigned a = __builtin_amdgcn_readfirstlane(lds_base);
-    asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(voff), "s"(sbase), "s"(a) : "memory");
-}
-
 // ---- LDS tiles ------------------------------------------------------------------------------------------
 
 // A tile of 32 rows of CH 16-byte chunks; chunk c of row r lies at slot c ^ key(r).  A pass of LDS reads covers 256
@@ -180,7 +173,7 @@ struct DTileCopy {
             for (int k = 0; k < kK; ++k) {
                 const int q = wave + NW * k;
                 if (kI % NW != 0 && q >= kI) break;
-                dma16_at(base, off[kPlan ? k : 0], lds + q * 1024u);
+                dma16_off(base, off[kPlan ? k : 0], lds + q * 1024u);
             }
         } else {
             for (int q = wave; q < kI; q += NW) {
@@ -188,7 +181,7 @@ struct DTileCopy {
                 place(q, lane, r, c);
                 if (c < valid) {
                     if (r < rows)
-                        dma16_at(base, (unsigned)r * row_bytes + 16u * c, lds + q * 1024u);
+                        dma16_off(base, (unsigned)r * row_bytes + 16u * c, lds + q * 1024u);
                     else
                         *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(lds + q * 1024u + lane * 16u) = u32x4{0, 0, 0, 0};
                 }
@@ -436,7 +429,7 @@ __device__ __forceinline__ void linear_copy(const unsigned char* src, unsigned l
 #pragma unroll
     for (int k = 0; k < ((BYTES + 1023) / 1024 + NW - 1) / NW; ++k) {
         const int q = wave + NW * k;
-        if (q * 1024 + lane * 16 < BYTES) dma16_at(src + q * 1024, lane * 16u, lds + q * 1024u);
+        if (q * 1024 + lane * 16 < BYTES) dma16_off(src + q * 1024, lane * 16u, lds + q * 1024u);
     }
 }
 

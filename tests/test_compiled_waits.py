@@ -3,7 +3,8 @@
 The kernels copy global memory to LDS by inline assembly, which the compiler's own count of wait states does not
 look into, so the disassembly is read back and every path through it is followed:
 
- * a copy to LDS takes its address from M0, and one wait state has to lie between a write of M0 and the copy.
+ * a copy to LDS takes its address from M0, and one wait state has to lie between a write of M0 and the copy;
+ * M0 is not the kernels' to keep: each copy's block saves it and puts it back.
 """
 import os
 import re
@@ -97,3 +98,14 @@ def test_copies_to_lds_wait_for_their_address(code):
                 assert not body[k].is_copy, (name, hex(body[k].at))
         seen += sum(i.is_copy for i in body)
     assert seen > 1000
+
+
+def test_copies_to_lds_restore_m0(code):
+    for name, body in code.items():
+        for n, i in enumerate(body):
+            if not i.is_copy:
+                continue
+            back = body[n + 1]
+            assert (back.op, back.args[0]) == ("s_mov_b32", "m0"), (name, hex(i.at))
+            save = [(j.op, j.args) for j in body[n - 3:n]]
+            assert save[0] == ("s_mov_b32", [back.args[1], "m0"]) and save[2][0] == "s_nop", (name, hex(i.at))
