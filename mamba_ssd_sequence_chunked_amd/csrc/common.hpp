@@ -115,6 +115,17 @@ __device__ __forceinline__ void mma(f32x4& acc, const Vec8<float>& a, const Vec8
     for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[i], b.v[i], acc, 0, 0, 0);
 }
 
+// Between matrix instructions and a branch behind which their results are read.  The hardware does not hold
+// back an instruction that reads a result too early: 8 wait states have to pass behind a bf16 product's
+// instruction and 10 behind an fp32 one's.  The compiler counts them, but where a short and a long path from
+// one block meet again it has been seen to count the long one only (two states too few on the short one),
+// so the longest wait is spent before the branch.
+__device__ __forceinline__ void settle() {
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("s_nop 15");
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // An fp32 value as a pair of bf16 values: hi = bf16(v), lo = bf16(v - hi) (v - hi is exact in fp32),
 // so |v - hi - lo| <= 2^-9 |v - hi| <= 2^-18 |v| (normal range).  A product with a bf16-valued
 // operand then takes two bf16 matrix-core products, hi and lo, instead of the fp32 ones.

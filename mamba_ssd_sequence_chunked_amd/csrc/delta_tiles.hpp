@@ -366,15 +366,6 @@ template <> struct Pair<float> {
     Vec8<float> hi;
     __device__ __forceinline__ void set(const float (&v)[8]) { pack8(hi, v); }
 };
-// Between matrix instructions and a branch behind which their results are read: the compiler's count of the wait states
-// that they need was seen to fall short across the branch (a conversion read two of four result registers too
-// early), so the longest wait is spent before it.
-__device__ __forceinline__ void settle()
-{
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("s_nop 15");
-    __builtin_amdgcn_sched_barrier(0);
-}
 
 // a exact, b a pair and the other way round; both pairs: without the product of the two low parts (2^-18), or with it
 __device__ __forceinline__ void mma_px(f32x4& acc, const Pair<bf16>& a, const Vec8<bf16>& b) { mma(acc, a.lo, b); mma(acc, a.hi, b); }

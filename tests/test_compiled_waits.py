@@ -4,7 +4,9 @@ The kernels copy global memory to LDS by inline assembly, which the compiler's o
 look into, so the disassembly is read back and every path through it is followed:
 
  * a copy to LDS takes its address from M0, and one wait state has to lie between a write of M0 and the copy;
- * M0 is not the kernels' to keep: each copy's block saves it and puts it back.
+ * M0 is not the kernels' to keep: each copy's block saves it and puts it back;
+ * a matrix instruction's result is not there for other units until 8 wait states (16 x 16 x 32 in bf16, four passes)
+   or 10 (16 x 16 x 4 in fp32, eight passes) have gone by, on whatever path the reader is reached.
 """
 import os
 import re
@@ -109,3 +111,65 @@ def test_copies_to_lds_restore_m0(code):
             assert (back.op, back.args[0]) == ("s_mov_b32", "m0"), (name, hex(i.at))
             save = [(j.op, j.args) for j in body[n - 3:n]]
             assert save[0] == ("s_mov_b32", [back.args[1], "m0"]) and save[2][0] == "s_nop", (name, hex(i.at))
+
+
+# wait states behind a matrix instruction before another unit may touch its result
+PASSES = {"v_mfma_f32_16x16x32_bf16": 8, "v_mfma_f32_16x16x4_f32": 10}
+
+
+def _touched(i):
+    """(registers read or written by another unit than the matrix cores, registers written)."""
+    every = [registers(a) for a in i.args]
+    if i.op.startswith("v_mfma"):
+        return every[1] + every[2], every[0]             # (an accumulator passed on is the matrix cores' own affair)
+    if i.op.startswith(("v_", "ds_")) or i.is_memory:
+        out = every[0] if i.op.startswith("v_") or "load" in i.op or "read" in i.op else []
+        return sum(every, []), out
+    return [], []
+
+
+def _waits(body, start, end, pending, seen=None):
+    """Follows a block from {register: wait states still to pass}; returns what is pending behind it."""
+    now, due = 0, {r: n for r, n in pending.items()}
+    for i in body[start:end]:
+        touched, written = _touched(i)
+        if seen is not None:
+            for r in touched:
+                if r[0] in "va" and due.get(r, 0) > now:
+                    seen.append((i, r, due[r] - now))
+        for r in written:
+            due.pop(r, None)
+        now += i.states
+        if i.op.startswith("v_mfma"):
+            need = PASSES.get(i.op, PASSES.get(i.op.rsplit("_e64", 1)[0], 18))
+            for r in written:
+                due[r] = now + need
+    return {r: t - now for r, t in due.items() if t > now}
+
+
+def test_matrix_results_are_waited_for(code):
+    kernels = 0
+    for name, body in code.items():
+        if not any(i.op.startswith("v_mfma") for i in body):
+            continue
+        kernels += 1
+        heads = sorted({0} | {k for n, i in enumerate(body) if i.target is not None for k in (*i.succ, n + 1)} - {len(body)})
+        end = dict(zip(heads, heads[1:] + [len(body)]))
+        entry, todo = {0: {}}, [0]
+        while todo:
+            h = todo.pop()
+            out = _waits(body, h, end[h], entry[h])
+            for k in body[end[h] - 1].succ:
+                old = entry.get(k)
+                new = dict(old or {})
+                for r, n in out.items():
+                    new[r] = max(new.get(r, 0), n)
+                if new != old:
+                    entry[k] = new
+                    todo.append(k)
+        early = []
+        for h in heads:
+            if h in entry:
+                _waits(body, h, end[h], entry[h], early)
+        assert not early, (name, [(i.op, hex(i.at), r, n) for i, r, n in early[:3]])
+    assert kernels > 100
