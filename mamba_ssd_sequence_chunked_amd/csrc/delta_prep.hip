@@ -160,6 +160,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(
                 mma(ak, a, b);
                 mma(aq, q, b);
             }
+            settle();                                     // they are read behind the branch
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) {

@@ -128,7 +128,7 @@ def _touched(i):
     return [], []
 
 
-def _waits(body, start, end, pending, seen=None):
+def _waits(body, start, end, pending, passes, seen=None):
     """Follows a block from {register: wait states still to pass}; returns what is pending behind it."""
     now, due = 0, {r: n for r, n in pending.items()}
     for i in body[start:end]:
@@ -141,10 +141,33 @@ def _waits(body, start, end, pending, seen=None):
             due.pop(r, None)
         now += i.states
         if i.op.startswith("v_mfma"):
-            need = PASSES.get(i.op, PASSES.get(i.op.rsplit("_e64", 1)[0], 18))
+            need = passes.get(i.op, passes.get(i.op.rsplit("_e64", 1)[0], 18))
             for r in written:
                 due[r] = now + need
     return {r: t - now for r, t in due.items() if t > now}
+
+
+def early_uses(body, passes):
+    """[(instruction, register, wait states missing)] over every path."""
+    heads = sorted({0} | {k for n, i in enumerate(body) if i.target is not None for k in (*i.succ, n + 1)} - {len(body)})
+    end = dict(zip(heads, heads[1:] + [len(body)]))
+    entry, todo = {0: {}}, [0]
+    while todo:
+        h = todo.pop()
+        out = _waits(body, h, end[h], entry[h], passes)
+        for k in body[end[h] - 1].succ:
+            old = entry.get(k)
+            new = dict(old or {})
+            for r, n in out.items():
+                new[r] = max(new.get(r, 0), n)
+            if new != old:
+                entry[k] = new
+                todo.append(k)
+    early = []
+    for h in heads:
+        if h in entry:
+            _waits(body, h, end[h], entry[h], passes, early)
+    return early
 
 
 def test_matrix_results_are_waited_for(code):
@@ -153,23 +176,18 @@ def test_matrix_results_are_waited_for(code):
         if not any(i.op.startswith("v_mfma") for i in body):
             continue
         kernels += 1
-        heads = sorted({0} | {k for n, i in enumerate(body) if i.target is not None for k in (*i.succ, n + 1)} - {len(body)})
-        end = dict(zip(heads, heads[1:] + [len(body)]))
-        entry, todo = {0: {}}, [0]
-        while todo:
-            h = todo.pop()
-            out = _waits(body, h, end[h], entry[h])
-            for k in body[end[h] - 1].succ:
-                old = entry.get(k)
-                new = dict(old or {})
-                for r, n in out.items():
-                    new[r] = max(new.get(r, 0), n)
-                if new != old:
-                    entry[k] = new
-                    todo.append(k)
-        early = []
-        for h in heads:
-            if h in entry:
-                _waits(body, h, end[h], entry[h], early)
+        early = early_uses(body, PASSES)
         assert not early, (name, [(i.op, hex(i.at), r, n) for i, r, n in early[:3]])
     assert kernels > 100
+
+
+def test_group_products_wait_before_the_branch(code):
+    """The products of a group's keys and queries are read behind a loop whose length is not known and a branch: the
+    longest wait, 16 states, is spent before it, whatever the compiler counts."""
+    kernels = 0
+    for name, body in code.items():
+        if "delta_prep" in name:
+            kernels += 1
+            early = [e for e in early_uses(body, {op: 16 for op in PASSES}) if e[0].op.startswith("ds_write")]
+            assert not early, (name, [(i.op, hex(i.at), r, n) for i, r, n in early[:3]])
+    assert kernels == 4
