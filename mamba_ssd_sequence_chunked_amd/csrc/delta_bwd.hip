@@ -65,6 +65,9 @@ __device__ __forceinline__ f32x4 raw_f32(u32x2 v)
 }
 __device__ __forceinline__ f32x4 raw_f32(u32x4 v) { return __builtin_bit_cast(f32x4, v); }
 
+// The stores before and behind this stay instructions of their own (a wait counts them).
+__device__ __forceinline__ void own_store() { asm volatile("" ::: "memory"); }
+
 template <typename T, int NB, int NW>
 __device__ __forceinline__ void walk_back(
     const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ dfinal,
@@ -204,6 +207,8 @@ __device__ __forceinline__ void walk_back(
     auto step = [&](int c, auto stage) __attribute__((always_inline)) {
         constexpr int b = decltype(stage)::value;
         // (see the walk forward; the loads ahead of the next block were started before its copies)
+        // Behind the last copy lie this many stores of the block before, each at least one instruction: own_store()
+        // stands between those that could become one.
         constexpr int kStores = 5;
         if (c < nblk - 1) wait_vmem_below<kStores>(); else wait_vmem();
         __syncthreads();
@@ -302,6 +307,7 @@ __device__ __forceinline__ void walk_back(
             const f32x4 vf = raw_f32(vv[t]);
             vd[t] = wt[0] * vf[0] + wt[1] * vf[1] + wt[2] * vf[2] + wt[3] * vf[3];
             buffer_store4(odv, perm32(t, r) * (int)vrow + 4 * g * (int)sizeof(T), 0, wt, T());
+            own_store();
         }
         // lane group g: dv . v (g even) or w . e of tile g / 2
         back.sums[(((pt * d.seqs + s) * d.nheads + h) * 2 + (g & 1)) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =

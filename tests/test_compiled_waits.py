@@ -6,7 +6,9 @@ look into, so the disassembly is read back and every path through it is followed
  * a copy to LDS takes its address from M0, and one wait state has to lie between a write of M0 and the copy;
  * M0 is not the kernels' to keep: each copy's block saves it and puts it back;
  * a matrix instruction's result is not there for other units until 8 wait states (16 x 16 x 32 in bf16, four passes)
-   or 10 (16 x 16 x 4 in fp32, eight passes) have gone by, on whatever path the reader is reached.
+   or 10 (16 x 16 x 4 in fp32, eight passes) have gone by, on whatever path the reader is reached;
+ * the walk back of the gated delta rule waits for a stage's copies by their place in line: at most 5 later memory
+   operations may be outstanding, so at least 5 have to lie behind the last copy, on every path.
 """
 import os
 import re
@@ -191,3 +193,48 @@ def test_group_products_wait_before_the_branch(code):
             early = [e for e in early_uses(body, {op: 16 for op in PASSES}) if e[0].op.startswith("ds_write")]
             assert not early, (name, [(i.op, hex(i.at), r, n) for i, r, n in early[:3]])
     assert kernels == 4
+
+
+def test_walk_back_counts_its_stores(code):
+    kernels = 0
+    for name, body in code.items():
+        if "delta_rev" not in name:
+            continue
+        before = {}
+        for n, i in enumerate(body):
+            for k in i.succ:
+                before.setdefault(k, []).append(n)
+        if not any(i.op == "s_barrier" for i in body):
+            continue                     # one wavefront: nothing tells this wait from the compiler's own
+        waits = []
+        for n, i in enumerate(body):
+            if i.op == "s_waitcnt" and "vmcnt(5)" in i.args[0]:
+                k = n + 1
+                while body[k].op.startswith(("s_", "v_")) and body[k].op != "s_barrier" and body[k].target is None:
+                    k += 1
+                if body[k].op == "s_barrier":            # (the compiler's own waits stand before an operand's use)
+                    waits.append(n)
+        assert waits, name
+        kernels += 1
+        # the copies of the loop (the one block copied before it is waited for with everything else)
+        inside, todo = set(waits), list(waits)
+        while todo:
+            new = [k for k in body[todo.pop()].succ if k not in inside]
+            inside.update(new)
+            todo += new
+        for w in waits:
+            fewest, todo, ends = {w: 0}, [w], []
+            while todo:
+                n = todo.pop()
+                for p in before.get(n, []):
+                    if p not in inside:
+                        continue
+                    if body[p].is_copy:
+                        ends.append(fewest[n])
+                        continue
+                    c = fewest[n] + body[p].is_memory
+                    if c < fewest.get(p, 99):
+                        fewest[p] = c
+                        todo.append(p)
+            assert ends and min(ends) >= 5, (name, hex(body[w].at), ends)
+    assert kernels >= 12
