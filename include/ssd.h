@@ -319,7 +319,9 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *     rows being batch or nseq (for ssd_delta_step batch * nheads < 2^24).  There is no chunk size.
  *   - With bf16 inputs the final states and the fp32 gradients keep fp32's accuracy (about 1e-5 of their
  *     norm, twice that where all keys of a row are alike): every fp32 operand of a matrix-core product
- *     that reaches them is carried as a pair of bf16 values.
+ *     that reaches them is carried as a pair of bf16 values.  For dg that is each head's own norm, however
+ *     strong its decay (a few times more in a head of a few dozen tokens whose final state has a gradient), unless what
+ *     it is summed from cancels, as where one unit key is written again and again with beta 1.
  *   - Non-finite inputs: the sums run over blocks of 32 tokens in which a later token's values carry a
  *     weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of the same
  *     32-token block of its sequence (and all later ones), never another sequence, batch row or group.
@@ -360,7 +362,8 @@ int ssd_delta_forward_varlen(const void* v, const float* g, const float* beta, c
  *   dv T like v; dg, dbeta float like g; dk, dq T like k (summed over a group's heads, in a fixed order);
  *   dinit float (batch, nheads, headdim, dstate), written also when init_states is NULL
  *   workspace of at least ssd_delta_backward_workspace_bytes() bytes
- * dg at the first token is 0 without an initial state (nothing decays into it). */
+ * dg at the first token is 0 without an initial state (nothing decays into it), and 0 at every token with g below -104
+ * (exp(g) is below fp32's range: nothing of the state passes). */
 size_t ssd_delta_backward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                                           int64_t dstate, int64_t ngroups, int dtype);
 int ssd_delta_backward(const void* v, const float* g, const float* beta, const void* k, const void* q,

@@ -7,25 +7,32 @@
 //   W = (dY U^T) o G (j <= i)           Z = -(w U^T) o diag(beta) G (j < i)
 //   dQ = diag(gam) dY S + W K           dK = W^T Q + (Z + Z^T) K + diag(del) U H - diag(beta gam) w S
 //
-// and for the log decay, whose gradient is <dL/dS'_t, S'_t>, the identity
+// and for the log decay, whose gradient is <dL/dS'_t, S'_t>,
 //
-//   dg_t = dg_{t+1} + dy_t . y_t - dv_t . v_t,     dg after a block's last token = <H, S>
+//   dg_t = dg_{t+1} + l_t,   l_t = dy_t . (S'_t q_t) - dv_t . (S'_t k_t) - u_t . (D_t k_t),   D_t = dL/dS_t without y_t's part
 //
-// so it needs row sums only, and the inner product of the two states at the ends of every 64-token chunk: a longer
-// sum's rounding errors would outgrow the gradient, which the decay keeps to a few tokens' size. The sum from a
-// chunk's end misses the value at its start by the errors of its 64 terms; the difference is spread evenly over them
-// (the error left at a token then is that of a bridge between two known ends, a third of the walk's variance).
+// (after a block's last token dg is <H, S>), so it needs row sums only, and the inner product of the two states at the
+// ends of every 64-token chunk. Every term of l_t is a product of what lies before token t and what lies behind it, so
+// a strong decay makes the terms small with the gradient. (The shorter l_t = dy_t . y_t - dv_t . v_t is the same number,
+// but its products within the token cancel: with g = -8 throughout, 1e-3 of dg's norm is lost even in fp32.) With S' k = x
+// from the walk forward, e = v - x, w' = D k = dU' + (B - I)^T dU, where dU' = dU - diag(q . k) dY, and w = w' +
+// diag(q . k) dY: l = dy . (S' q) - beta (w . x + e . w').
 //
-// Four steps: the records (delta_prep); the walk forward again (delta_fwd.hip), keeping e, dy . y and the state
+// The sum from a chunk's end and the sum from its start differ by the errors of the 64 terms and the two inner products.
+// dg_t is the mean of both, each weighted with the other's squared terms (the errors go with the terms): a bridge between two
+// known ends, and where an end is large and the gradient is not, as at a last token with a strong decay and a
+// gradient of the final state, the sum from the other end. Where S' is zero in fp32 (g below -104) dg is 0.
+//
+// Four steps: the records (delta_prep); the walk forward again (delta_fwd.hip), keeping x, dy . S' q and the state
 // at every 64th token; the walk back (below), the same form with H in the state's place; and, for all chunks of 64
 // tokens at once, dq and dk, summed over the heads that share them inside a workgroup, in a fixed order.
 // Everything that leads to H, dbeta and dg is computed on pairs (fp32's accuracy for bf16 inputs); dq and dk,
 // which are rounded to T themselves, on T.
 //
 // What bounds it: the kept states and values, about 5.5 GB written and read at 4 x 4096 tokens, 80 heads of 64 x 128
-// (bf16), 1.83 ms in all: records 139 us, walk forward 594, walk back 722 (2.3 GB, 3.2 TB/s), dq and dk 387 (1.3 GB,
-// 3.5 TB/s), their sums 8, dg and dbeta 25. A chunk of 64 tokens is what dg's accuracy asks for; the walk back copies with
-// its own wavefronts, as one that feeds them took 742 us.
+// (bf16), 1.91 ms in all: records 148 us, walk forward 627, walk back 747 (2.3 GB, 3.1 TB/s), dq and dk 442 (1.5 GB,
+// 3.4 TB/s), their sums 8, dg and dbeta 32. (With l_t from y and v, 1.83: 145, 613, 733, 403, 8, 26.) A chunk of 64
+// tokens is what dg's accuracy asks for; the walk back copies with its own wavefronts, as one that feeds them took 3 % longer.
 #include <type_traits>
 
 #include "delta_tiles.hpp"
@@ -38,8 +45,8 @@ constexpr int kChunk = 64;       // tokens of a chunk of the dq, dk step
 
 // What the walk back keeps, beside DeltaKeep.
 template <typename T> struct DeltaBack {
-    T* w;                    // as e: w of every block, head and 16 columns
-    float* sums;             // (headdim / 16, seqs, nheads, 2, 64 chunks): dv . v and w . e over 16 columns
+    T* w;                    // as x: w of every block, head and 16 columns
+    float* sums;             // (headdim / 16, seqs, nheads, 2, 64 chunks): beta (w . x + e . w') and w . e over 16 columns
     T* H;                    // (seqs, chunks, nheads): dL/d(state after each 64-token chunk), as fragments
     float* hs;               // (headdim / 16, seqs, chunks + 1, nheads): <H, S> over 16 rows at the chunks' ends
 };
@@ -67,6 +74,15 @@ __device__ __forceinline__ f32x4 raw_f32(u32x4 v) { return __builtin_bit_cast(f3
 
 // The stores before and behind this stay instructions of their own (a wait counts them).
 __device__ __forceinline__ void own_store() { asm volatile("" ::: "memory"); }
+
+// Row `row`'s columns c .. c + 3 (c a multiple of 4) of a VTile.
+template <typename T, int CH>
+__device__ __forceinline__ f32x4 vtile_row4(unsigned tile, int row, int c)
+{
+    constexpr int kPer = 16 / (int)sizeof(T);
+    typedef decltype(load_raw(static_cast<const T*>(nullptr))) Raw;
+    return raw_f32(lds_at<Raw>(tile + VTile<CH>::offset(row, c / kPer) + (c % kPer) * (int)sizeof(T)));
+}
 
 template <typename T, int NB, int NW>
 __device__ __forceinline__ void walk_back(
@@ -184,20 +200,20 @@ __device__ __forceinline__ void walk_back(
         dot = group_sum<64>(dot);
         if (lane == 0) back.hs[((pt * d.seqs + s) * (keep.chunks + 1) + k) * d.nheads + h] = dot;
     };
-    // v and e of this lane's tokens and 4 columns in the columns = tokens form, fetched a block ahead
+    // v and x of this lane's tokens and 4 columns in the columns = tokens form, fetched a block ahead
     Raw vv[2], vn[2];
-    f32x4 ev[2], en[2];
-    auto fetch_ve = [&](int c) __attribute__((always_inline)) {
+    f32x4 xv[2], xn[2];
+    auto fetch_vx = [&](int c) __attribute__((always_inline)) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             const int64_t tok = sq.start + min(c * kDC + perm32(t, r), sq.len - 1);
             vn[t] = load_raw(v + (tok * d.nheads + h) * P + 16 * pt + 4 * g);
-            en[t] = *reinterpret_cast<const f32x4*>(keep.e + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g));
+            xn[t] = *reinterpret_cast<const f32x4*>(keep.x + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g));
         }
     };
     if (nblk > 0) {
         fetch_S((nblk + 1) / 2);
-        fetch_ve(nblk - 1);
+        fetch_vx(nblk - 1);
     } else {
         fetch_S(0);
     }
@@ -231,10 +247,10 @@ __device__ __forceinline__ void walk_back(
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             vv[t] = vn[t];
-            ev[t] = en[t];
+            xv[t] = xn[t];
         }
         if (c > 0) {
-            fetch_ve(c - 1);
+            fetch_vx(c - 1);
             issue(c - 1, 1 - b);
         }
         const unsigned st = lds0 + b * C::kStage, rec = st + C::kR - R::kM, tab = rec + R::kTab;
@@ -273,45 +289,54 @@ __device__ __forceinline__ void walk_back(
                 mma_xp(kh[t], kf, hp);
             }
         }
-        float dU[8];
+        // dU' is without M's diagonal, dU with it
+        float dU[8], dO[8], qk8[8];
+        tab_rows(qk8, tab + 384, g);
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
             for (int m = 0; m < 4; ++m) du[t][m] = kh[t][m] * de[4 * t + m];
             mma_px(du[t], mt[t], yf);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) dU[4 * t + m] = du[t][m];
+            for (int m = 0; m < 4; ++m) {
+                dO[4 * t + m] = du[t][m];
+                dU[4 * t + m] = fmaf(qk8[4 * t + m], yf.get(4 * t + m), du[t][m]);
+            }
         }
-        Pair<T> dup;
+        Pair<T> dup, dop;
         dup.set(dU);
+        dop.set(dO);
         // w = B^T dU in both forms: rows tokens (to go on with) and columns tokens (to hand out). Rows past the
         // sequence are outside the buffers: dropped.
         const int64_t th = (sq.start + c * kDC) * d.nheads + h;
         const auto odv = __builtin_amdgcn_make_buffer_rsrc(dv + th * P + 16 * pt, 0, (rows - 1) * (int)vrow + 16 * (int)sizeof(T), kBufferDword3);
-        float we[2], vd[2];
+        float we[2], ll[2];
         float bw[8];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
             Vec8<T> one;
             unit_frag(one, t, r, g);
-            f32x4 w = du[t], wt = {0.f, 0.f, 0.f, 0.f};
+            f32x4 w = {dU[4 * t], dU[4 * t + 1], dU[4 * t + 2], dU[4 * t + 3]}, wo = {0.f, 0.f, 0.f, 0.f};
             mma_pp<true>(w, bm[t], dup);
-            mma_pp<true>(wt, dup, bm[t]);
-            mma_rest(wt, dup, dU, one);
-            mma_px(wt, dup, one);
+            mma_pp<true>(wo, dup, bm[t]);
+            mma_rest(wo, dop, dO, one);
+            mma_px(wo, dop, one);
+            const float qk = lds_at<float>(tab + 384 + 4 * perm32(t, r));
+            f32x4 wt = wo + qk * vtile_row4<T, C::kCV>(st + C::kY, perm32(t, r), 16 * wave + 4 * g);
 #pragma unroll
             for (int m = 0; m < 4; ++m) bw[4 * t + m] = -ga[4 * t + m] * bt8[4 * t + m] * w[m];
             store4(back.w + keep.frag(sq.slot + c, h, pt, d) + keep.lane(perm32(t, r), g), wt[0], wt[1], wt[2], wt[3]);
-            we[t] = wt[0] * ev[t][0] + wt[1] * ev[t][1] + wt[2] * ev[t][2] + wt[3] * ev[t][3];
+            const f32x4 ev = raw_f32(vv[t]) - xv[t];
+            we[t] = wt[0] * ev[0] + wt[1] * ev[1] + wt[2] * ev[2] + wt[3] * ev[3];
+            ll[t] = bet[t] * (wt[0] * xv[t][0] + wt[1] * xv[t][1] + wt[2] * xv[t][2] + wt[3] * xv[t][3] +
+                              wo[0] * ev[0] + wo[1] * ev[1] + wo[2] * ev[2] + wo[3] * ev[3]);
             wt *= bet[t];
-            const f32x4 vf = raw_f32(vv[t]);
-            vd[t] = wt[0] * vf[0] + wt[1] * vf[1] + wt[2] * vf[2] + wt[3] * vf[3];
             buffer_store4(odv, perm32(t, r) * (int)vrow + 4 * g * (int)sizeof(T), 0, wt, T());
             own_store();
         }
-        // lane group g: dv . v (g even) or w . e of tile g / 2
+        // lane group g: beta (w . x + e . w') (g even) or w . e of tile g / 2
         back.sums[(((pt * d.seqs + s) * d.nheads + h) * 2 + (g & 1)) * keep.chunks * 64 + c * kDC + perm32(g >> 1, r)] =
-            sum_groups(vd[0], vd[1], we[0], we[1]);
+            sum_groups(ll[0], ll[1], we[0], we[1]);
         // H before the block = gam_last H + Q^T (gam dY) - K^T (beta gam w)
         float gy[8];
 #pragma unroll
@@ -361,8 +386,9 @@ __global__ __launch_bounds__(64 * NW) void delta_rev_f32_kernel(
 // A wavefront = one 64-token chunk of one head, lane = token; a workgroup = that chunk of 16 heads, whose results are
 // turned in LDS so that they leave as pieces of token rows.
 __global__ __launch_bounds__(256) void delta_scalar_kernel(
-    const float* __restrict__ ydy, const float* __restrict__ sums, const float* __restrict__ hs, float* __restrict__ dg,
-    float* __restrict__ dbeta, DeltaDims d, int64_t chunks, int hblocks, int zero_first)
+    const float* __restrict__ ydy, const float* __restrict__ sums, const float* __restrict__ hs,
+    const float* __restrict__ gv, float* __restrict__ dg, float* __restrict__ dbeta, DeltaDims d, int64_t chunks,
+    int hblocks, int zero_first)
 {
     __shared__ float og[64][17], ob[64][17];
     const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
@@ -373,28 +399,39 @@ __global__ __launch_bounds__(256) void delta_scalar_kernel(
     for (int i = wave; i < 16; i += 4) {
         const int h = h0 + i;
         if (h >= d.nheads) break;
-        float loc = 0.f, b = 0.f;
-        double start = 0.0, end = 0.0;
+        float b = 0.f;
+        // the sums, and in 16 columns each, their squares: what the weights are made of
+        double loc = 0.0, loc2 = 0.0, start = 0.0, start2 = 0.0, end = 0.0, end2 = 0.0;
         for (int pt = 0; pt < npt; ++pt) {
             const int64_t row = (pt * d.seqs + s) * d.nheads + h;
             if (lane < left) {
                 const float* at = sums + row * 2 * chunks * 64 + k * 64 + lane;
-                loc += ydy[row * chunks * 64 + k * 64 + lane] - at[0];
+                const double p = ydy[row * chunks * 64 + k * 64 + lane], q = at[0];
+                loc += p - q;
+                loc2 += (fabs(p) + fabs(q)) * (fabs(p) + fabs(q));
                 b += at[chunks * 64];
             }
             const float* e = hs + ((pt * d.seqs + s) * (chunks + 1) + k) * d.nheads + h;
-            start += e[0];
-            end += e[d.nheads];
+            const double e0 = e[0], e1 = e[d.nheads];
+            start += e0;
+            start2 += e0 * e0;
+            end += e1;
+            end2 += e1 * e1;
         }
-        // sums from this token to the chunk's end
-        double run = loc;
+        // sums from this token to the chunk's end, and from the chunk's start to before it
+        double down = loc, down2 = loc2, up = loc, up2 = loc2;
 #pragma unroll
         for (int m = 1; m < 64; m <<= 1) {
-            const double down = __shfl_down(run, m, 64);
-            if (lane + m < 64) run += down;
+            const double a = __shfl_down(down, m, 64), a2 = __shfl_down(down2, m, 64);
+            const double c = __shfl_up(up, m, 64), c2 = __shfl_up(up2, m, 64);
+            if (lane + m < 64) { down += a; down2 += a2; }
+            if (lane >= m) { up += c; up2 += c2; }
         }
-        const double miss = (start - end - __shfl(run, 0, 64)) / left;
-        og[lane][i] = (float)(end + run + miss * (left - lane));
+        up = __shfl_up(up, 1, 64);
+        up2 = __shfl_up(up2, 1, 64);
+        const double from_end = end + down, from_start = lane ? start - up : start;
+        const double w_start = end2 + down2, w_end = lane ? start2 + up2 : start2;
+        og[lane][i] = (float)(w_start + w_end > 0.0 ? (from_start * w_start + from_end * w_end) / (w_start + w_end) : from_end);
         ob[lane][i] = b;
     }
     __syncthreads();
@@ -402,8 +439,8 @@ __global__ __launch_bounds__(256) void delta_scalar_kernel(
         const int t = j / 16, i = j % 16;
         if (t < left && h0 + i < d.nheads) {
             const int64_t at = (s * d.seqlen + k * 64 + t) * d.nheads + h0 + i;
-            // without an initial state nothing decays into the first token
-            dg[at] = zero_first && k == 0 && t == 0 ? 0.f : og[t][i];
+            // without an initial state nothing decays into the first token, and nothing into one that resets the state
+            dg[at] = (zero_first && k == 0 && t == 0) || gv[at] < -104.f ? 0.f : og[t][i];
             dbeta[at] = ob[t][i];
         }
     }
@@ -427,8 +464,8 @@ struct KqCfg {
 // tokens and all N columns of dq and dk (as rows n, columns = tokens).
 template <typename T, int NB>
 __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
-    const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ gv, const float* __restrict__ bv,
-    DeltaKeep<T> keep, DeltaBack<T> back, T* __restrict__ dq, T* __restrict__ dk, float* __restrict__ partial,
+    const T* __restrict__ v, const T* __restrict__ Km, const T* __restrict__ Qm, const float* __restrict__ gv,
+    const float* __restrict__ bv, DeltaKeep<T> keep, DeltaBack<T> back, T* __restrict__ dq, T* __restrict__ dk, float* __restrict__ partial,
     DeltaDims d, int nslice)
 {
     using C = KqCfg<T, NB>;
@@ -499,17 +536,21 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
         copy_state(back.H + ((s * keep.chunks + k) * d.nheads + h) * keep.plane(d) + off, rows, st + C::kTile);
     };
     // the operands of a stage in registers: lane = token, slots = columns {4g .., 16 + 4g ..} of 32
-    struct Ops { float4 y[2], e[2], w[2]; float gr, be; };
+    typedef decltype(load_raw(static_cast<const T*>(nullptr))) Raw;
+    struct Ops { float4 y[2], x[2], w[2]; Raw v[2]; float gr, be; };
     auto fetch = [&](int i) __attribute__((always_inline)) {
         Ops o;
         const int h = h0 + i / nkb, kb = i % nkb;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-            o.y[t] = o.e[t] = o.w[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+            o.y[t] = o.x[t] = o.w[t] = make_float4(0.f, 0.f, 0.f, 0.f);
+            o.v[t] = Raw{};
             if (tok && blk && 32 * kb + 16 * t < P) {
-                o.y[t] = load4f(keep.dy + ((t0 + mine) * d.nheads + h) * P + 32 * kb + 16 * t + 4 * g);
+                const int64_t at = ((t0 + mine) * d.nheads + h) * P + 32 * kb + 16 * t + 4 * g;
+                o.y[t] = load4f(keep.dy + at);
+                o.v[t] = load_raw(v + at);
                 const int64_t f = keep.frag(slot, h, 2 * kb + t, d) + (wave & 1) * 256 + lane * 4;
-                o.e[t] = load4f(keep.e + f);
+                o.x[t] = load4f(keep.x + f);
                 o.w[t] = load4f(back.w + f);
             }
         }
@@ -543,7 +584,10 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
         const float gam = __expf((float)ci), del = __expf((float)(cst[wave][63] - ci)), be = bet[wave][mine];
         float f[8];
         const float yv[8] = {cur.y[0].x, cur.y[0].y, cur.y[0].z, cur.y[0].w, cur.y[1].x, cur.y[1].y, cur.y[1].z, cur.y[1].w};
-        const float ev[8] = {cur.e[0].x, cur.e[0].y, cur.e[0].z, cur.e[0].w, cur.e[1].x, cur.e[1].y, cur.e[1].z, cur.e[1].w};
+        const float xv[8] = {cur.x[0].x, cur.x[0].y, cur.x[0].z, cur.x[0].w, cur.x[1].x, cur.x[1].y, cur.x[1].z, cur.x[1].w};
+        const f32x4 v0 = raw_f32(cur.v[0]), v1 = raw_f32(cur.v[1]);
+        const float ev[8] = {v0[0] - xv[0], v0[1] - xv[1], v0[2] - xv[2], v0[3] - xv[3],
+                             v1[0] - xv[4], v1[1] - xv[5], v1[2] - xv[6], v1[3] - xv[7]};
         const float wv[8] = {cur.w[0].x, cur.w[0].y, cur.w[0].z, cur.w[0].w, cur.w[1].x, cur.w[1].y, cur.w[1].z, cur.w[1].w};
         Vec8<T> yf, wf, gy, du, bw, uf;
         pack8(yf, yv);
@@ -709,7 +753,7 @@ int kq_slices(const DeltaDims& d)
     return (int)(want < hpg / 2 ? want : hpg / 2 > 1 ? hpg / 2 : 1);
 }
 
-struct BwdSpace { size_t rec, e, w, ydy, sums, S, Slo, H, hs, part, total; };
+struct BwdSpace { size_t rec, x, w, ydy, sums, S, Slo, H, hs, part, total; };
 
 BwdSpace bwd_space(const DeltaDims& d, size_t es)
 {
@@ -720,7 +764,7 @@ BwdSpace bwd_space(const DeltaDims& d, size_t es)
     size_t at = 0;
     auto put = [&](size_t bytes) { const size_t here = at; at += (bytes + 255) / 256 * 256; return here; };
     b.rec = put(slots * heads * (es == 2 ? DeltaRec<bf16, true>::kBytes : DeltaRec<float, true>::kBytes));
-    b.e = put(slots * heads * npt * 512 * 4);
+    b.x = put(slots * heads * npt * 512 * 4);
     b.w = put(slots * heads * npt * 512 * es);
     b.ydy = put(npt * th * 4);
     b.sums = put(npt * th * 2 * 4);
@@ -765,7 +809,7 @@ hipError_t launch_nb(const T* v, const float* g, const float* beta, const T* k, 
     if (e != hipSuccess || d.seqlen == 0) return e;
     const int ns = kq_slices(d);
     hipLaunchKernelGGL((delta_kq_kernel<T, NB>), dim3((unsigned)(d.seqs * keep.chunks * d.ngroups * ns)), dim3(256), 0,
-                       stream, k, q, g, beta, keep, back, dq, dk, partial, d, ns);
+                       stream, v, k, q, g, beta, keep, back, dq, dk, partial, d, ns);
     e = hipGetLastError();
     if (e != hipSuccess || ns == 1) return e;
     const int64_t n4 = d.tokens * d.ngroups * d.dstate / 4;
@@ -790,7 +834,7 @@ hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, 
     auto f = [&](size_t at) { return reinterpret_cast<float*>(ws + at); };
     auto t = [&](size_t at) { return reinterpret_cast<T*>(ws + at); };
     const int64_t chunks = (d.seqlen + kChunk - 1) / kChunk;
-    const DeltaKeep<T> keep{dy, f(b.e), f(b.ydy), t(b.S), t(b.Slo), chunks};
+    const DeltaKeep<T> keep{dy, f(b.x), f(b.ydy), t(b.S), t(b.Slo), chunks};
     const DeltaBack<T> back{t(b.w), f(b.sums), t(b.H), f(b.hs)};
     hipError_t e = launch_delta_prep<T, true>(k, q, g, beta, ws + b.rec, d, stream);
     if (e == hipSuccess)
@@ -807,7 +851,7 @@ hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, 
     if (e != hipSuccess || d.seqlen == 0) return e;
     const int hblocks = (int)((d.nheads + 15) / 16);
     hipLaunchKernelGGL(delta_scalar_kernel, dim3((unsigned)(d.seqs * chunks * hblocks)), dim3(256), 0, stream, keep.ydy,
-                       back.sums, back.hs, dg, dbeta, d, chunks, hblocks, init == nullptr ? 1 : 0);
+                       back.sums, back.hs, g, dg, dbeta, d, chunks, hblocks, init == nullptr ? 1 : 0);
     return hipGetLastError();
 }
 

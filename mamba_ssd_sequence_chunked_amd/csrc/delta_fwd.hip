@@ -14,10 +14,11 @@
 // the 2-norm, of which its own rounding is 1.7e-3. (U is a pair there too, at 2 more matrix instructions a block: 2.8e-3
 // without. S as one would cost 8 and 6 % of the time, for 0.1e-3.)
 //
-// kBwd is the backward's walk forward: the same block by block, with y kept to fp32's accuracy (pairs there too)
-// and, in place of y and the final state, what the walk back and the gradients of k and q need (DeltaKeep). dg is
-// the small difference of dy . y and dv . v, so what these are made of is carried further: the low parts' product and
-// the third bf16 piece of E and U take its error from 7e-6 to 4.6e-6, with decays down to e^-40 from 2.8e-5 to 7e-6.
+// kBwd is the backward's walk forward: the same block by block, in place of y and the final state leaving what the
+// walk back and the gradients of k and q need (DeltaKeep). The log decays' gradients need the decayed state's answers
+// S' q and S' k to fp32's accuracy of their own (delta_bwd.hip): S' q is y without the token's own update (M below
+// its diagonal), S' k = gam K S^T - (A - I) E, neither the difference of larger numbers, on pairs with the low parts'
+// product and the third bf16 piece of U and K S^T.
 //
 // A workgroup = NW wavefronts that walk (16 rows each, of one head or of NH next to each other) and one that feeds
 // them: K, Q, the V columns and the blocks' records come through a ring of kBuf stages of asynchronous global -> LDS
@@ -221,21 +222,35 @@ __device__ __forceinline__ void chain(
         for (int i = 0; i < 8; ++i) E[i] = vf.get(i) - gam8[i] * ks[i >> 2][i & 3];
         Pair<T> ep, du;
         ep.set(E);
+        if constexpr (kBwd) {
+            float ks8[8];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-            f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
-            mma_pp<kBwd>(e, am[t], ep);
+            for (int i = 0; i < 8; ++i) ks8[i] = gam8[i] * ks[i >> 2][i & 3];
+            Pair<T> kp;
+            kp.set(ks8);
 #pragma unroll
-            for (int m = 0; m < 4; ++m) e8[4 * t + m] = e[m];
-            if constexpr (kBwd) {
-                // e once more with columns = tokens, the form in which it is kept
+            for (int t = 0; t < 2; ++t) {
+                f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
+                mma_pp<true>(e, am[t], ep);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) e8[4 * t + m] = e[m];
+                // x = S' k with columns = tokens, the form in which it is kept
                 Vec8<T> one;
                 unit_frag(one, t, r, g);
-                f32x4 et = {0.f, 0.f, 0.f, 0.f};
-                mma_pp<true>(et, ep, am[t]);
-                mma_rest(et, ep, E, one);
-                mma_px(et, ep, one);
-                store4(keep.e + keep.frag(sq.slot + c, h, pv / 16, d) + keep.lane(perm32(t, r), g), et[0], et[1], et[2], et[3]);
+                f32x4 xt = {0.f, 0.f, 0.f, 0.f};
+                mma_pp<true>(xt, ep, am[t]);
+                xt = -xt;
+                mma_rest(xt, kp, ks8, one);
+                mma_px(xt, kp, one);
+                store4(keep.x + keep.frag(sq.slot + c, h, pv / 16, d) + keep.lane(perm32(t, r), g), xt[0], xt[1], xt[2], xt[3]);
+            }
+        } else {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f32x4 e = {E[4 * t], E[4 * t + 1], E[4 * t + 2], E[4 * t + 3]};
+                mma_pp(e, am[t], ep);
+#pragma unroll
+                for (int m = 0; m < 4; ++m) e8[4 * t + m] = e[m];
             }
         }
         // U = beta e (the forward's records have beta in M and in del)

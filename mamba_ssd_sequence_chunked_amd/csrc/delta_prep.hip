@@ -223,7 +223,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(
                             const int j = 16 * J + 4 * g + m;
                             const float G = __builtin_amdgcn_exp2f((float)(ci - cj[m]));
                             const bool in = i < rows && j < rows;
-                            M[m] = in && i >= j ? G * q4[m] * (kBwd ? 1.f : bj[m]) : 0.f;
+                            M[m] = in && (kBwd ? i > j : i >= j) ? G * q4[m] * (kBwd ? 1.f : bj[m]) : 0.f;
+                            if constexpr (kBwd) {
+                                if (i == j && out) reinterpret_cast<float*>(out + R::kTab)[96 + i] = in ? q4[m] : 0.f;
+                            }
                             X[e][I + J][m] = in && i > j ? G * k4[m] : 0.f;
                             lt[e * 32 * kLd + j * kLd + i] = X[e][I + J][m] * bj[m];
                         }

@@ -84,8 +84,8 @@ __device__ __forceinline__ bool delta_slot(const DeltaDims& d, int64_t slot, Del
 // plane, and tables of 32 floats.  A and B are kept without their unit diagonals: what they multiply is added in
 // fp32, so that a rounding of the pairs counts for the rest only.
 //   forward:  A - I (hi, lo), M diag(beta) (hi only), tables gam, del beta
-//   backward: A - I, M (both as pairs), tables gam, del, beta, B - I with B = (I + diag(beta) X)^-1 (pair); the walk
-//             forward reads A to the tables, the walk back M to B
+//   backward: A - I, M below its diagonal (both as pairs), tables gam, del, beta and M's diagonal q_i . k_i, B - I with
+//             B = (I + diag(beta) X)^-1 (pair); the walk forward reads A to the tables, the walk back M to B
 template <typename T, bool kBwd> struct DeltaRec {
     static constexpr int kPair = sizeof(T) == 2 ? 2 : 1;
     static constexpr int kMat = 32 * 32 * (int)sizeof(T);
@@ -436,8 +436,9 @@ __device__ __forceinline__ void tab_rows(float (&v)[8], unsigned tab, int g)
 
 template <typename T> struct DeltaKeep {
     const T* dy;
-    float* e;                // e of every block, head and 16 columns: (2 x 16 tokens) as 64 lanes (4 columns, token) x 4
-    float* ydy;              // (headdim / 16, seqs, nheads, 64 chunks): dy . y over 16 columns
+    float* x;                // x = S' k = v - e of every block, head and 16 columns: (2 x 16 tokens) as 64 lanes (4
+                             //   columns, token) x 4
+    float* ydy;              // (headdim / 16, seqs, nheads, 64 chunks): dy . S' q over 16 columns
     T* S;                    // (seqs, chunks + 1, nheads): the state entering each 64-token chunk, and after the last, as
     T* Slo;                  //   fragments (state_at); for bf16 also what the rounding to T drops
     int64_t chunks;          // 64-token chunks of a row
