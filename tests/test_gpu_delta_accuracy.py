@@ -6,12 +6,25 @@ Tolerances, fixed before the first run:
    so that errors of one term add up at random to at most 8 of them.  For bf16 inputs the term's operands are pairs of
    bf16 values, off by at most 2^-18 each, two to a product: 2^-17.  For fp32 inputs a term sums products over N and
    64 more values, whose half steps of 2^-24 add up at random: sqrt(N + 64) of them.
+ * A rounding's error is spread evenly over its half step: 1 / sqrt(3) of it in the mean.  Roundings of different values
+   add up at random, so a sum's error is counted in the root of its terms' squares.
+ * y: for bf16 inputs its own rounding, the state's and the scores' to bf16 (each rounded once where it leads to y);
+   for both types 4 times the fp32 unit: the products' sums, and those of the state that they are made from.  A score q . k
+   is a sum of N products itself: rounded to bf16 it is off by half a step of its value, but as an fp32 sum by half steps
+   of its terms (with |q . k| = 0.004 of unit vectors, fp32's half step of the terms' 1 / sqrt(N) is 2e-6 of the value), so
+   the fp32 unit counts a score's terms and not its value.
+ * dv: its own rounding; dk, dq: four, their own and those of a product's two operands in two products.
+ * final states, dbeta, dg, dinit for bf16 inputs: the header's 1e-5 of the norm.  Where all keys of a row are alike and
+   beta is 1, a block's 32 updates are differences of values, sqrt(2) as large as the values, and add up to one of
+   them, so what is left of their 32 roundings (2^-18, of pairs) is sqrt(32) sqrt(2) = 8 of them; dk and dq then sum 64 such
+   updates rounded to bf16: sqrt(64) sqrt(2) roundings.
 """
 import numpy as np
 import pytest
 
 import delta_ref as ref
-from test_gpu_delta import dev, f64, grads, inputs
+from test_gpu_delta import CASES, GRADS, ROUND, VARLEN, dev, f64, grads, ident, inputs, rel2
+from test_gpu_delta_guard import MANY
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +93,110 @@ def test_log_decay_gradient_of_a_reset_is_zero(dt, reset):
     assert (got[at] == 0).all()
     want = ref.backward(d["v"], d["g"], d["beta"], d["k"], d["q"], d["dy"], d["init"], d["dfinal"])["dg"]
     assert per_head(got, want) <= dg_unit(dt, 64)
+
+
+# ---- y, final states and the other gradients, in the 2-norm -----------------------------------------
+
+def fp32_unit(N):
+    return np.sqrt(N + 64) * 2.0 ** -24
+
+
+def mean_rounding(dtype):
+    return ROUND[dtype] / np.sqrt(3)
+
+
+def y_size(v, g, beta, k, q, init=None):
+    """The roots of the squares of y's terms, like y: the entering state's products with q, the block's scores' with its
+    updates, and y itself; and the same with the products that a score is summed from in the score's place."""
+    b, L, H, P = v.shape
+    K, Q = ref.heads(k, H), ref.heads(q, H)
+    S = np.zeros((b, H, P, k.shape[3])) if init is None else init.copy()
+    out, fine = np.zeros_like(v), np.zeros_like(v)
+    for t in range(L):
+        if t % ref.BLOCK == 0:
+            S0, us, ks = S, [], []
+        a = np.exp(g[:, t])[:, :, None]
+        S0 = a[..., None] * S0
+        us = [a * u for u in us]
+        Sp = a[..., None] * S
+        kt, qt = K[:, t, :, None, :], Q[:, t, :, None, :]
+        u = beta[:, t, :, None] * (v[:, t] - (Sp * kt).sum(-1))
+        S = Sp + u[..., None] * kt
+        us.append(u)
+        ks.append(K[:, t])
+        out[:, t] = ((S0 * qt) ** 2).sum(-1) + (S * qt).sum(-1) ** 2
+        fine[:, t] = out[:, t]
+        for uj, kj in zip(us, ks):
+            out[:, t] += ((Q[:, t] * kj).sum(-1)[..., None] * uj) ** 2
+            fine[:, t] += ((Q[:, t] * kj) ** 2).sum(-1)[..., None] * uj ** 2
+    return np.sqrt(out), np.sqrt(fine)
+
+
+def check_y(y, want, size, dtype, N):
+    """Each row and head for itself."""
+    err, room, fine = (np.linalg.norm(np.moveaxis(a, 2, 1).reshape(a.shape[0], a.shape[2], -1), axis=-1)
+                       for a in (f64(y) - want, *size))
+    tol = 4 * fp32_unit(N) * fine + (mean_rounding("bf16") * room if dtype == "bf16" else 0.0)
+    print(f"y {(err / np.maximum(tol, 1e-300)).max(initial=0):.2f} of its tolerance", flush=True)
+    assert (err <= tol).all()
+
+
+def state_tolerance(dtype, N, kind):
+    if dtype == "f32":
+        return 8 * fp32_unit(N)
+    return 8 * 2.0 ** -18 if kind == "repeat" else 1e-5
+
+
+REPEATS = [
+    (1, 300, 4, 64, 128, 2, "bf16", False, "repeat"),
+    (2, 95, 3, 128, 64, 1, "bf16", True, "repeat"),
+    (1, 160, 4, 16, 256, 4, "bf16", True, "repeat"),
+]
+
+
+@pytest.mark.parametrize("c", CASES + MANY + REPEATS, ids=ident)
+def test_forward_accuracy(c):
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, L, H, P, N, G, dt, init, kind = c
+    d = ref.make(b, L, H, P, N, G, dt, init, seed=1300 + L, kind=kind)
+    x = [d[n] for n in ("v", "g", "beta", "k", "q", "init")]
+    y, fin = ssd.delta_forward(*inputs(d), dev(d["init"]))
+    want = ref.forward(*x)
+    check_y(y, want[0], y_size(*x), dt, N)
+    e = rel2(f64(fin), want[1])
+    print(f"final {e:.2e}", flush=True)
+    assert e <= state_tolerance(dt, N, kind)
+
+
+@pytest.mark.parametrize("c", VARLEN, ids=lambda c: "n{}_T{}_H{}_P{}_N{}_G{}_{}_{}".format(len(c[0]), sum(c[0]), *c[1:]))
+def test_varlen_accuracy(c):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    lens, H, P, N, G, dt, init = c
+    d = ref.make(1, sum(lens), H, P, N, G, dt, False, seed=1400 + sum(lens))
+    h0 = 0.3 * np.random.default_rng(4).standard_normal((len(lens), H, P, N)) if init else None
+    h0 = None if h0 is None else h0.astype(np.float32).astype(np.float64)
+    cu = np.concatenate([[0], np.cumsum(lens)])
+    y, fin = ssd.delta_forward_varlen(*(t[0] for t in inputs(d)), torch.tensor(cu, dtype=torch.int32, device="cuda"), dev(h0))
+    for i in range(len(lens)):
+        x = [d[n][:, cu[i]:cu[i + 1]] for n in ("v", "g", "beta", "k", "q")] + [None if h0 is None else h0[i:i + 1]]
+        want = ref.forward(*x)
+        check_y(y[None, cu[i]:cu[i + 1]], want[0], y_size(*x), dt, N)
+        e = rel2(f64(fin[i:i + 1]), want[1])
+        assert e <= state_tolerance(dt, N, "layer") if want[1].any() else not f64(fin[i]).any(), (i, e)
+
+
+@pytest.mark.parametrize("c", GRADS + REPEATS[1:], ids=ident)
+def test_backward_accuracy(c):
+    b, L, H, P, N, G, dt, init, kind = c
+    d = ref.make(b, L, H, P, N, G, dt, init, seed=1500 + L, kind=kind)
+    got = grads(d)
+    want = ref.backward(d["v"], d["g"], d["beta"], d["k"], d["q"], d["dy"], d["init"], d["dfinal"])
+    for n, w in want.items():
+        tol = state_tolerance(dt, N, kind)
+        if dt == "bf16" and n in ("dv", "dk", "dq"):
+            many = 1 if n == "dv" else 8 * np.sqrt(2) if kind == "repeat" else 2
+            tol += many * mean_rounding("bf16")
+        e = rel2(f64(got[n]), w)
+        print(f"{n} {e:.2e} of {tol:.2e}", flush=True)
+        assert e <= tol if w.any() else not f64(got[n]).any(), n
