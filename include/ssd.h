@@ -329,6 +329,7 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *   - Non-finite inputs: the sums run over blocks of 32 tokens in which a later token's values carry a
  *     weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of the same
  *     32-token block of its sequence (and all later ones), never another sequence, batch row or group.
+ *     ssd_delta_backward sums over chunks of 64: beside the gradients that depend on the token, all of its chunk's.
  * ------------------------------------------------------------------------------------------- */
 
 /* y, final_states of the gated delta rule over whole sequences.

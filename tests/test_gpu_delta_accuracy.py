@@ -200,3 +200,24 @@ def test_backward_accuracy(c):
         e = rel2(f64(got[n]), w)
         print(f"{n} {e:.2e} of {tol:.2e}", flush=True)
         assert e <= tol if w.any() else not f64(got[n]).any(), n
+
+
+def test_backward_confines_what_is_not_finite():
+    """A NaN in dy reaches the gradients before it and those of its chunk of 64 tokens, in its row and group only."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(2, 200, 4, 64, 64, 2, "bf16", True, seed=1600)
+    x, dy = inputs(d), dev(d["dy"], "bf16")
+    a = ssd.delta_backward(*x, dy, dev(d["init"]), dev(d["dfinal"]))
+    dy[1, 70, 3] = float("nan")                  # group 1: heads 2 and 3
+    b = ssd.delta_backward(*x, dy, dev(d["init"]), dev(d["dfinal"]))
+    for n in a:
+        assert torch.equal(a[n][0], b[n][0]), n
+        if n == "dinit":
+            assert torch.equal(a[n][1, :3], b[n][1, :3]) and torch.isnan(b[n][1, 3]).all()
+            continue
+        own = slice(1, None) if n in ("dk", "dq") else slice(3, None)
+        rest = slice(0, own.start)
+        assert torch.equal(a[n][1, :, rest], b[n][1, :, rest]), n
+        assert torch.equal(a[n][1, 128:], b[n][1, 128:]), n
+    assert torch.isnan(b["dv"][1, :71, 3]).all()
