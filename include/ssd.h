@@ -338,7 +338,8 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *   init_states float (batch, nheads, headdim, dstate) or NULL (zeros)
  *   y T like v, written; final_states float (batch, nheads, headdim, dstate), written: the state after the
  *     last token (the initial one when seqlen = 0)
- *   workspace of at least ssd_delta_forward_workspace_bytes() bytes (0 = the sizes or dtype are refused) */
+ *   workspace of at least ssd_delta_forward_workspace_bytes() bytes (0 = the sizes or dtype are refused): 6.5 KB
+ *     (fp32 8.5) for every 32 tokens of a row and head; 0.27 GB at 4 x 4096 tokens and 80 heads in bf16 */
 size_t ssd_delta_forward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                                          int64_t dstate, int64_t ngroups, int dtype);
 int ssd_delta_forward(const void* v, const float* g, const float* beta, const void* k, const void* q,
@@ -366,7 +367,8 @@ int ssd_delta_forward_varlen(const void* v, const float* g, const float* beta, c
  *   dy T like v; dfinal float (batch, nheads, headdim, dstate) or NULL
  *   dv T like v; dg, dbeta float like g; dk, dq T like k (summed over a group's heads, in a fixed order);
  *   dinit float (batch, nheads, headdim, dstate), written also when init_states is NULL
- *   workspace of at least ssd_delta_backward_workspace_bytes() bytes
+ *   workspace of at least ssd_delta_backward_workspace_bytes() bytes: for bf16 inputs 2.1 GB at 4 x 4096 tokens, 80
+ *     heads of 64 x 128; 12.4 GB at 65536 tokens, 80 heads of 64 x 256 (mostly the states kept every 64 tokens)
  * dg at the first token is 0 without an initial state (nothing decays into it), and 0 at every token with g below -104
  * (exp(g) is below fp32's range: nothing of the state passes). */
 size_t ssd_delta_backward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,

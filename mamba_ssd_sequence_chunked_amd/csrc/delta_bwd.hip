@@ -29,10 +29,11 @@
 // Everything that leads to H, dbeta and dg is computed on pairs (fp32's accuracy for bf16 inputs); dq and dk,
 // which are rounded to T themselves, on T.
 //
-// What bounds it: the kept states and values, about 5.5 GB written and read at 4 x 4096 tokens, 80 heads of 64 x 128
-// (bf16), 1.91 ms in all: records 148 us, walk forward 627, walk back 747 (2.3 GB, 3.1 TB/s), dq and dk 442 (1.5 GB,
-// 3.4 TB/s), their sums 8, dg and dbeta 32. (With l_t from y and v, 1.83: 145, 613, 733, 403, 8, 26.) A chunk of 64
-// tokens is what dg's accuracy asks for; the walk back copies with its own wavefronts, as one that feeds them took 3 % longer.
+// What bounds it: the kept states and values, 7.2 GB written and read (counted) at 4 x 4096 tokens, 80 heads of 64 x 128
+// (bf16), 1.91 ms in all: records 145 us (0.64 GB), walk forward 618 (1.9 GB, 3.1 TB/s), walk back 738 (2.5 GB, 3.4 TB/s),
+// dq and dk 435 (2.0 GB, 4.6 TB/s), their sums 8, dg and dbeta 31. (With l_t from y and v, 1.83: 145, 613, 733, 403, 8, 26.)
+// A chunk of 64 tokens is what dg's accuracy asks for; the walk back copies with its own wavefronts, as one that feeds
+// them took 3 % longer when both were measured.
 #include <type_traits>
 
 #include "delta_tiles.hpp"

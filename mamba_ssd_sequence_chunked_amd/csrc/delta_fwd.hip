@@ -24,7 +24,7 @@
 // them: K, Q, the V columns and the blocks' records come through a ring of kBuf stages of asynchronous global -> LDS
 // copies, all issued by that one. A wavefront that issues copies stalls while they queue up (28 KB a block at 64
 // bytes a cycle), which cost the walk a fifth of its time when its own wavefronts did (192 heads of 64 x 128 over
-// 2048 tokens: 74 us against 91). One barrier per block.
+// 2048 tokens: 74 us against 91, before U was a pair in y; now 79). One barrier per block.
 // What bounds it: the chain of one block's products, about 2900 cycles of which a wavefront's matrix instructions
 // fill 800 and its vector instructions 900; two wavefronts on a SIMD take 4600 a block. Measured (with U a pair in y):
 // 320 heads over 4096 tokens 245 us, 192 over 2048 79, 80 of 64 x 256 over 65536 3490.
@@ -363,9 +363,10 @@ hipError_t launch_nw(const T* v, const T* k, const T* q, const float* init, cons
     if constexpr (sizeof(T) == 2 && NB <= 4) {
         // More workgroups of 64 columns than CUs, and a second one does not fit a CU beside the first (its five
         // wavefronts would put four on one SIMD): eight wavefronts that share K and Q, two heads of 64 columns or one
-        // of 128. 320 heads of 64 x 128 over 4096 tokens: 226 us against 273; 7 sequences of 64 to 4096 tokens, 80
-        // heads: 224 against 249; 37 of 1 to 150, 16 heads of 128 x 128: 40 against 46. With fewer, four: 192 heads over
-        // 2048 tokens take 75 us.
+        // of 128. Whole calls, records included: 320 heads of 64 x 128 over 4096 tokens 298 us against 345 with four
+        // (their backward 1913 against 2070); 7 sequences of 64 to 4096 tokens, 80 heads, 288 against 314; 37 of 1 to
+        // 150, 16 heads of 128 x 128, 51 against 58. With fewer, four: 192 heads over 2048 tokens 104 against 143 with
+        // eight, their backward 614 against 692.
         constexpr int64_t kCUs = 256;
         if (d.seqs * d.nheads * d.headdim > 64 * kCUs) {
             if (d.headdim == 128) SSD_CHAIN(8, 1);

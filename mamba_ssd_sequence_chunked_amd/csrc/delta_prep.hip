@@ -13,7 +13,7 @@
 // decay early in a block costs later pairs no digits.
 //
 // Bound by the records' bytes and by the substitutions' chain of 16 dependent rows: 4 x 4096 tokens, 80 heads
-// (bf16, N = 128) 85 us for 273 MB of records, 140 us for the backward's 524 MB. Forward substitution of whole 32 x 32
+// (bf16, N = 128) 85 us for 273 MB of records, 145 us for the backward's 524 MB. Forward substitution of whole 32 x 32
 // matrices took 140 us and 370.
 #include "delta_tiles.hpp"
 
