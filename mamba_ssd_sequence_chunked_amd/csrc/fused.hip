@@ -247,9 +247,9 @@ __global__ __launch_bounds__(kThreads) void ssd_fused_kernel(
                 }
             }
         }
-        settle();                                        // the state is read behind the branches below
         if (t0 + kTB < seqlen) tables(u ^ 1);           // the other set was last read before this block's barrier
         __syncthreads();                                 // every read of this block's tiles and state is done
+        settle();                                        // the state's products lie behind branches
         put_state();                                     // (read after the next block's barrier)
     }
 #pragma unroll
