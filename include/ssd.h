@@ -323,9 +323,9 @@ int ssd_selective_scan(const void* x, const float* delta, const float* A, const 
  *     strong its decay (a few times more in a head of a few dozen tokens whose final state has a gradient), unless what
  *     it is summed from cancels, as where one unit key is written again and again with beta 1.
  *   - The bf16 outputs are a little further off than their own rounding (1.7e-3 of the norm): y 2.4e-3, because the
- *     state and the scores are rounded to bf16 where they lead to y only, dk and dq 2.9e-3, dv 1.7e-3.  The roundings go
- *     with the terms of a sum: where these cancel, as with like keys, more of the sum is lost (y 4e-3 to 9e-3, dq
- *     7e-3 to 2e-2).  With fp32 inputs everything is fp32.
+ *     state and the scores are rounded to bf16 where they lead to y only, dk and dq 1.8e-3, dv 1.7e-3.  The roundings go
+ *     with the terms of a sum: where these cancel, as with like keys, more of the sum is lost (y 4e-3 to 9e-3, dk and
+ *     dq 2.5e-3 to 3e-3).  With fp32 inputs everything is fp32.
  *   - Non-finite inputs: the sums run over blocks of 32 tokens in which a later token's values carry a
  *     weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of the same
  *     32-token block of its sequence (and all later ones), never another sequence, batch row or group.

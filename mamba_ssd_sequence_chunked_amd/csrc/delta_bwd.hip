@@ -26,8 +26,11 @@
 // Four steps: the records (delta_prep); the walk forward again (delta_fwd.hip), keeping x, dy . S' q and the state
 // at every 64th token; the walk back (below), the same form with H in the state's place; and, for all chunks of 64
 // tokens at once, dq and dk, summed over the heads that share them inside a workgroup, in a fixed order.
-// Everything that leads to H, dbeta and dg is computed on pairs (fp32's accuracy for bf16 inputs); dq and dk,
-// which are rounded to T themselves, on T.
+// Everything that leads to H, dbeta and dg is computed on pairs (fp32's accuracy for bf16 inputs). dq and dk are rounded
+// to T themselves. For bf16 U, W and Z are pairs there too: their rounding was most of the error (2.9e-3 of the norm,
+// now 1.8e-3 of which dq's own rounding is 1.66e-3; with one key again and again, where the updates cancel, 1.8e-2 and
+// now 2.5e-3) and pairs cost 1 % of the time. S, H, w, gam dY, del U and beta gam w are rounded to bf16 once: the last three
+// as pairs leave 1.7e-3 for another 1 %, S's low part would be read for 4 %.
 //
 // What bounds it: the kept states and values, 7.2 GB written and read (counted) at 4 x 4096 tokens, 80 heads of 64 x 128
 // (bf16), 1.91 ms in all: records 145 us (0.64 GB), walk forward 618 (1.9 GB, 3.1 TB/s), walk back 738 (2.5 GB, 3.4 TB/s),
@@ -455,10 +458,11 @@ struct KqCfg {
     static constexpr int kTile = DTile<kCH>::kBytes;               // 32 rows of S, H, K or Q
     static constexpr int kStage = 2 * kTile;
     static constexpr int kCW = kChunk * (int)sizeof(T) / 16;       // chunks of a row of W or Z
-    static constexpr int kWz = 2 * DTile<kCW>::kBytes;             // W or Z: 64 rows
-    static constexpr int kEpi = 2 * kTile + 2 * kWz;
+    static constexpr int kWz = 2 * DTile<kCW>::kBytes;             // W or Z: 64 rows, a plane
+    static constexpr int kPlanes = sizeof(T) == 2 ? 2 : 1;         // of W, Z and U: pairs
+    static constexpr int kEpi = 2 * kTile + 2 * kPlanes * kWz;
     static constexpr int kRing = 2 * kStage > kEpi ? 2 * kStage : kEpi;
-    static constexpr int kU = 4 * 64 * 8 * (int)sizeof(T);         // U of 64 tokens x 32 columns as fragments
+    static constexpr int kU = kPlanes * 4 * 64 * 8 * (int)sizeof(T);   // U of 64 tokens x 32 columns as fragments
 };
 
 // A workgroup = one 64-token chunk of one (row, group) and a range of the group's heads; a wavefront = 16 of the
@@ -598,7 +602,8 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
         pack8(gy, f);
 #pragma unroll
         for (int m = 0; m < 8; ++m) f[m] = be * ev[m];
-        pack8(uf, f);
+        Pair<T> up;
+        up.set(f);
 #pragma unroll
         for (int m = 0; m < 8; ++m) f[m] *= del;
         pack8(du, f);
@@ -606,7 +611,8 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
         for (int m = 0; m < 8; ++m) f[m] = -be * gam * wv[m];
         pack8(bw, f);
         T* un = reinterpret_cast<T*>(ub[i & 1]) + (wave * 64 + lane) * 8;
-        store8(un, uf);
+        store8(un, up.hi);
+        if constexpr (sizeof(T) == 2) store8(un + 4 * 64 * 8, up.lo);
         wait_vmem();
         __syncthreads();
         if (i + 1 < nst) {
@@ -626,10 +632,11 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
 #pragma unroll
         for (int t = 0; t < 4; ++t) {
             if (t <= wave) {
-                Vec8<T> u;
-                load8(u, reinterpret_cast<const T*>(ub[i & 1]) + (t * 64 + lane) * 8);
-                mma(wa[t], yf, u);
-                mma(za[t], wf, u);
+                Pair<T> u;
+                load8(u.hi, reinterpret_cast<const T*>(ub[i & 1]) + (t * 64 + lane) * 8);
+                if constexpr (sizeof(T) == 2) load8(u.lo, reinterpret_cast<const T*>(ub[i & 1]) + 4 * 64 * 8 + (t * 64 + lane) * 8);
+                mma_xp(wa[t], yf, u);
+                mma_xp(za[t], wf, u);
             }
         }
         settle();
@@ -654,7 +661,7 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
     __syncthreads();
     // W and Z to LDS behind the place of K's two tiles (whose pad columns are zero still): dq += W K, dk += (Z + Z^T) K, then Q in K's place: dk += W^T Q
     unsigned char* const wl = ring + 2 * C::kTile;
-    unsigned char* const zl = wl + C::kWz;
+    unsigned char* const zl = wl + C::kPlanes * C::kWz;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
 #pragma unroll
@@ -663,8 +670,13 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
             constexpr int kPer = 16 / (int)sizeof(T);
             const int o = (wave >> 1) * DTile<C::kCW>::kBytes + DTile<C::kCW>::offset(row, col / kPer) +
                           (col % kPer) * (int)sizeof(T);
-            *reinterpret_cast<T*>(wl + o) = from_f32<T>(Ws[t][m]);
-            *reinterpret_cast<T*>(zl + o) = from_f32<T>(Zs[t][m]);
+            const T wh = from_f32<T>(Ws[t][m]), zh = from_f32<T>(Zs[t][m]);
+            *reinterpret_cast<T*>(wl + o) = wh;
+            *reinterpret_cast<T*>(zl + o) = zh;
+            if constexpr (C::kPlanes == 2) {
+                *reinterpret_cast<T*>(wl + C::kWz + o) = from_f32<T>(Ws[t][m] - to_f32(wh));
+                *reinterpret_cast<T*>(zl + C::kWz + o) = from_f32<T>(Zs[t][m] - to_f32(zh));
+            }
         }
     }
     DTileCopy<C::kCH, 4> kcopy;
@@ -682,30 +694,38 @@ __global__ __launch_bounds__(256, 2) void delta_kq_kernel(
     load_rows(Km);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        Vec8<T> wr, zr, zc;
-        wrows.load(wr, wl0 + (wave >> 1) * DTile<C::kCW>::kBytes, wave & 1, b);
-        wrows.load(zr, wl0 + C::kWz + (wave >> 1) * DTile<C::kCW>::kBytes, wave & 1, b);
-        DCols<T, C::kCW>::load_any(zc, wl0 + C::kWz + b * DTile<C::kCW>::kBytes, wave, r, g);
+        const unsigned wt = wl0 + (wave >> 1) * DTile<C::kCW>::kBytes, zt = wt + C::kPlanes * C::kWz;
+        const unsigned ct = wl0 + C::kPlanes * C::kWz + b * DTile<C::kCW>::kBytes;
+        Pair<T> wr, zr, zc;
+        wrows.load(wr.hi, wt, wave & 1, b);
+        wrows.load(zr.hi, zt, wave & 1, b);
+        DCols<T, C::kCW>::load_any(zc.hi, ct, wave, r, g);
+        if constexpr (C::kPlanes == 2) {
+            wrows.load(wr.lo, wt + C::kWz, wave & 1, b);
+            wrows.load(zr.lo, zt + C::kWz, wave & 1, b);
+            DCols<T, C::kCW>::load_any(zc.lo, ct + C::kWz, wave, r, g);
+        }
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             Vec8<T> kf;
             cols.load(kf, lds0 + b * C::kTile, t);
-            mma(aq[t], kf, wr);
-            mma(ak[t], kf, zr);
-            mma(ak[t], kf, zc);
+            mma_xp(aq[t], kf, wr);
+            mma_xp(ak[t], kf, zr);
+            mma_xp(ak[t], kf, zc);
         }
     }
     __syncthreads();
     load_rows(Qm);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
-        Vec8<T> wc;
-        DCols<T, C::kCW>::load_any(wc, wl0 + b * DTile<C::kCW>::kBytes, wave, r, g);
+        Pair<T> wc;
+        DCols<T, C::kCW>::load_any(wc.hi, wl0 + b * DTile<C::kCW>::kBytes, wave, r, g);
+        if constexpr (C::kPlanes == 2) DCols<T, C::kCW>::load_any(wc.lo, wl0 + C::kWz + b * DTile<C::kCW>::kBytes, wave, r, g);
 #pragma unroll
         for (int t = 0; t < 2 * NB; ++t) {
             Vec8<T> qf;
             cols.load(qf, lds0 + b * C::kTile, t);
-            mma(ak[t], qf, wc);
+            mma_xp(ak[t], qf, wc);
         }
     }
     settle();

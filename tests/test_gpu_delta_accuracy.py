@@ -221,3 +221,21 @@ def test_backward_confines_what_is_not_finite():
         assert torch.equal(a[n][1, :, rest], b[n][1, :, rest]), n
         assert torch.equal(a[n][1, 128:], b[n][1, 128:]), n
     assert torch.isnan(b["dv"][1, :71, 3]).all()
+
+
+@pytest.mark.parametrize("c", [c for c in GRADS if c[6] == "bf16" and c[1] > 1] + REPEATS, ids=ident)
+def test_key_and_query_gradients_accuracy(c):
+    """What a rounding to bf16 is off by in the mean, counted exactly: its half step is 2^-8 / m of a value of mantissa m,
+    the mean of 1 / m^2 over evenly spread logarithms 0.541, so 2^-8 sqrt(0.541 / 3) = 1.66e-3.  dk and dq are made of
+    two halves, what is left of the states and the chunk's own pairs of tokens: the first's two operands are rounded, the
+    second's are not, and the sum is, so 1.66e-3 sqrt(1 + 2 / 2).  Where all keys are alike the two halves cancel in
+    part: two roundings more."""
+    b, L, H, P, N, G, dt, init, kind = c
+    d = ref.make(b, L, H, P, N, G, dt, init, seed=1700 + L, kind=kind)
+    got = grads(d)
+    want = ref.backward(d["v"], d["g"], d["beta"], d["k"], d["q"], d["dy"], d["init"], d["dfinal"])
+    tol = 2.0 ** -8 * np.sqrt(0.541 / 3) * np.sqrt(4 if kind == "repeat" else 2)
+    for n in ("dk", "dq"):
+        e = rel2(f64(got[n]), want[n])
+        print(f"{n} {e:.2e} of {tol:.2e}", flush=True)
+        assert e <= tol, n
