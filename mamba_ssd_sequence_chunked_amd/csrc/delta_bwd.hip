@@ -33,8 +33,9 @@
 // as pairs leave 1.7e-3 for another 1 %, S's low part would be read for 4 %.
 //
 // What bounds it: the kept states and values, 7.2 GB written and read (counted) at 4 x 4096 tokens, 80 heads of 64 x 128
-// (bf16), 1.91 ms in all: records 145 us (0.64 GB), walk forward 618 (1.9 GB, 3.1 TB/s), walk back 738 (2.5 GB, 3.4 TB/s),
-// dq and dk 435 (2.0 GB, 4.6 TB/s), their sums 8, dg and dbeta 31. (With l_t from y and v, 1.83: 145, 613, 733, 403, 8, 26.)
+// (bf16), 1.94 ms in all: records 147 us (0.64 GB), walk forward 633 (1.9 GB, 3.0 TB/s), walk back 739 (2.5 GB, 3.4 TB/s),
+// dq and dk 448 (2.0 GB, 4.5 TB/s), their sums 8, dg and dbeta 31. (With l_t from y and v, and U, W, Z rounded once: 1.83,
+// of which 145, 613, 733, 403, 8, 26.)
 // A chunk of 64 tokens is what dg's accuracy asks for; the walk back copies with its own wavefronts, as one that feeds
 // them took 3 % longer when both were measured.
 #include <type_traits>
