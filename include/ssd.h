@@ -386,6 +386,104 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
                    void* y, int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
                    int dtype, void* stream);
 
+/* ---------------------------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the recurrence with a constant decay, a query per head, and keys and
+ * values that may be shared by the heads of a group (retention; grouped queries).
+ *
+ *     S_t = exp(g_h) S_{t-1} + v_t k_t^T      (state: headdim x dstate per head, as above)
+ *     y_t = S_t q_t
+ *
+ * q is a head's own; head h reads k and v of group h / (nheads / ngroups), ngroups = nheads where nothing is shared.
+ * Conventions and errors are those at the top of this header, and:
+ *   - g float (nheads) is the log decay, <= 0 and constant in time; it is not clamped, except that every g below
+ *     -1000 acts as -1000 (exp is 0 in fp32 from -104 on), so -inf leaves each token alone. g = 0 is plain causal
+ *     linear attention. No scale is applied to q.
+ *   - headdim and dstate are multiples of 16 in [16, 256]; nheads * headdim and nheads * dstate <= 2^20; 0 <= batch <=
+ *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
+ *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate
+ *     < 2^34, tokens * ngroups * the wider < 2^34; for ssd_linear_step batch * nheads * headdim < 2^28.
+ *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (1e-6 to 3e-6 of their norm): what leads to
+ *     them is carried as pairs of bf16 values. bf16 outputs are a little further off than their own rounding (1.7e-3 of the
+ *     norm), because the scores and, where they are read, the states are rounded to bf16 on the way: up to 2.6e-3.
+ *     With fp32 inputs everything is fp32.
+ *   - Sums are made in a fixed order: the same call gives the same bits.
+ *   - Non-finite inputs: tokens are summed in chunks of up to 64 (of their sequence or of a segment of it) in which later tokens
+ *     have a weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of its chunk (and all
+ *     later ones), of the heads that read it, never another sequence, batch row or group. A gradient's chunks go from the
+ *     end: there it can reach later tokens of the chunk and all earlier ones.
+ * ------------------------------------------------------------------------------------------- */
+
+/* y, final_states over whole sequences.
+ *   v T (batch, seqlen, ngroups, headdim); g float (nheads); k T (batch, seqlen, ngroups, dstate)
+ *   q T (batch, seqlen, nheads, dstate)
+ *   init_states float (batch, nheads, headdim, dstate) or NULL (zeros)
+ *   y T (batch, seqlen, nheads, headdim), written; final_states float (batch, nheads, headdim, dstate), written: the state
+ *     after the last token (the initial one when seqlen = 0)
+ *   workspace of at least ssd_linear_forward_workspace_bytes() bytes (0 = the sizes or dtype are refused): the states
+ *     between segments where few long rows are cut into segments, else 256 */
+size_t ssd_linear_forward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                          int64_t dstate, int64_t ngroups, int dtype);
+int ssd_linear_forward(const void* v, const float* g, const void* k, const void* q, const float* init_states, void* y,
+                       float* final_states, int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                       int64_t dstate, int64_t ngroups, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The same for a packed variable-length batch: sequence i is tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of one token
+ * axis; a sequence may continue from a state.
+ *   v T (total_tokens, ngroups, headdim); k T (total_tokens, ngroups, dstate); q T (total_tokens, nheads, dstate)
+ *   cu_seqlens int32 (nseq + 1), DEVICE memory, non-decreasing from 0 to total_tokens (empty sequences
+ *     allowed); content not checked, other content yields unspecified values but no access outside the buffers. Tokens
+ *     behind cu_seqlens[nseq] are no sequence's: their y is left as it was
+ *   init_states float (nseq, nheads, headdim, dstate) or NULL (zeros)
+ *   y T (total_tokens, nheads, headdim), written; final_states float (nseq, nheads, headdim, dstate), written */
+size_t ssd_linear_forward_varlen_workspace_bytes(int64_t total_tokens, int64_t nseq, int64_t nheads, int64_t headdim,
+                                                 int64_t dstate, int64_t ngroups, int dtype);
+int ssd_linear_forward_varlen(const void* v, const float* g, const void* k, const void* q, const int32_t* cu_seqlens,
+                              int64_t nseq, const float* init_states, void* y, float* final_states,
+                              int64_t total_tokens, int64_t nheads, int64_t headdim, int64_t dstate, int64_t ngroups,
+                              int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of ssd_linear_forward for dL/dy = dy and dL/d(final_states) = dfinal (NULL = 0).
+ *   dy T like y; dfinal float (batch, nheads, headdim, dstate) or NULL
+ *   dv, dk T like v, k: summed over the heads of a group, in their order, and rounded once; dq T like q
+ *   dg float (nheads): summed over tokens and batch rows, 0 where g is below -104 (and without rows)
+ *   dinit float (batch, nheads, headdim, dstate), written also when init_states is NULL
+ *   workspace of at least ssd_linear_backward_workspace_bytes() bytes: with shared keys and values an fp32 copy of every
+ *     head's dk and dv, else the states between segments and a few sums */
+size_t ssd_linear_backward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
+                                           int64_t dstate, int64_t ngroups, int dtype);
+int ssd_linear_backward(const void* v, const float* g, const void* k, const void* q, const float* init_states,
+                        const void* dy, const float* dfinal, void* dv, float* dg, void* dk, void* dq, float* dinit,
+                        int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim, int64_t dstate,
+                        int64_t ngroups, int dtype, void* workspace, size_t workspace_bytes, void* stream);
+
+/* One token, the states advanced IN PLACE.
+ *   state float (nslots, nheads, headdim, dstate); v T (batch, ngroups, headdim); k T (batch, ngroups, dstate)
+ *   q T (batch, nheads, dstate); y T (batch, nheads, headdim), written
+ *   slots int32 (batch), DEVICE memory, or NULL (then nslots = batch, row i's state is state[i]): row i's state is
+ *     state[slots[i]]. A row whose slot is out of range (padding: -1) touches no state and gets y = 0, and so
+ *     does a row whose slot an earlier row has. States that no row names are left as they were. */
+int ssd_linear_step(float* state, const int32_t* slots, int64_t nslots, const void* v, const float* g, const void* k,
+                    const void* q, void* y, int64_t batch, int64_t nheads, int64_t headdim, int64_t dstate,
+                    int64_t ngroups, int dtype, void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * Pools of states. A server keeps the states of ssd_step, ssd_delta_step or ssd_linear_step in slots of a pool, one
+ * sequence a slot: copying, forking, reordering, compacting and freeing them is one map of slots,
+ *
+ *     states[l, i] = source[l, src[i]]   where 0 <= src[i] < nsource
+ *     states[l, i] = 0                   where src[i] = -1 (freed)
+ *     states[l, i] stays                 for any other src[i]
+ *
+ * for every layer l. With source NULL it works IN PLACE: every slot takes what src[i] held before the call, whatever
+ * the map (beams reordered, one prompt forked to many, live slots moved together), and src[i] = i leaves a slot alone.
+ *   states float (nlayers, nslots, slot_floats), read (in place) and written
+ *   source float (nlayers, nsource, slot_floats) or NULL (then nsource = nslots): for instance the final states of a prefill
+ *   src int32 (nslots), DEVICE memory; any content is safe
+ * No workspace. 0 <= nlayers <= 65535; 0 <= nslots <= 65535, in place at most 2048; nsource <= 2^24; slot_floats (nheads *
+ * headdim * dstate) a multiple of 4, at most 2^32. The values are copied as they are, NaN included. */
+int ssd_state_move(float* states, const float* source, const int32_t* src, int64_t nlayers, int64_t nslots,
+                   int64_t nsource, int64_t slot_floats, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -191,4 +191,29 @@ hipError_t launch_delta_backward(const T* v, const float* g, const float* beta, 
                                  T* dk, T* dq, float* dinit, const DeltaDims& d, void* workspace, hipStream_t stream);
 size_t delta_backward_workspace(const DeltaDims& d, int elem_bytes);
 
+// ---- linear attention with a decay for each head (the "linear" entry points) and pools of states ------
+
+// (DeltaDims, with k and v shared by the heads of a group and q a head's own)
+template <typename T>
+hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T* q, const float* init, T* y,
+                                 float* fin, const DeltaDims& d, void* workspace, hipStream_t stream);
+size_t linear_forward_workspace(const DeltaDims& d, int elem_bytes);
+
+template <typename T>
+hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const T* q, const float* init, const T* dy,
+                                  const float* dfinal, T* dv, float* dg, T* dk, T* dq, float* dinit, const DeltaDims& d,
+                                  void* workspace, hipStream_t stream);
+size_t linear_backward_workspace(const DeltaDims& d, int elem_bytes);
+// the most workgroups that any of their kernels is started with
+int64_t linear_blocks(const DeltaDims& d, int elem_bytes);
+
+// slots: each row's slot in a pool of nslots states, or null (row i's is i)
+template <typename T>
+hipError_t launch_linear_step(float* state, const int32_t* slots, int64_t nslots, const T* v, const float* g, const T* k,
+                              const T* q, T* y, const DeltaDims& d, hipStream_t stream);
+
+// source null: the pool itself
+hipError_t launch_state_move(float* states, const float* source, const int32_t* src, int64_t nlayers, int64_t nslots,
+                             int64_t nsource, int64_t slot_floats, hipStream_t stream);
+
 }  // namespace ssd

@@ -1,0 +1,290 @@
+// linear.hip - linear attention with a decay for each head: the forward and the backward as walks (linear_walk.hpp), and
+// the small kernels between and behind them.
+//
+// The forward is one walk.  The backward is three: dq forwards, with the sums of dg; dk and dv backwards.  Where there are
+// fewer walks than the GPU holds, rows are cut into segments: a first pass leaves what every segment but the last adds to
+// the state, linear_join_kernel turns that into the states that enter them, and the walk runs over all segments
+// at once.
+#include <algorithm>
+
+#include "linear_walk.hpp"
+
+namespace ssd {
+
+namespace {
+
+// What enters every segment, from what each adds (loc, in place; with dloc the derivative for g too).  A thread
+// has 4 elements of a row and head and goes along the row.
+//   S_0 = init;  S_{i+1} = a^len S_i + loc_i;   S'_0 = 0;  S'_{i+1} = a^len (S'_i + len S_i) + dloc_i
+template <bool kDg>
+__global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ loc, float* __restrict__ dloc,
+                                                          const float* __restrict__ init, const float* __restrict__ g,
+                                                          DeltaDims d, int64_t seg, bool back, int64_t PN)
+{
+    const int64_t quads = PN / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= d.seqs * d.nheads * quads) return;
+    const int64_t at = 4 * (i % quads), rh = i / quads, h = rh % d.nheads, row = rh / d.nheads;
+    int64_t first, n;
+    if (d.cu) {
+        const int64_t begin = linear_offset(d, row), end = max(linear_offset(d, row + 1), begin);
+        first = begin / seg + row;
+        n = end - begin;
+    } else {
+        first = row * max((d.seqlen + seg - 1) / seg, (int64_t)1);
+        n = d.seqlen;
+    }
+    const int64_t count = max((n + seg - 1) / seg, (int64_t)1);
+    const float gl = fmaxf(g[h], -1000.f);
+    f32x4 s = {0.f, 0.f, 0.f, 0.f}, ds = {0.f, 0.f, 0.f, 0.f};
+    if (init) s = *reinterpret_cast<const f32x4*>(init + rh * PN + at);
+    for (int64_t c = 0; c < count; ++c) {
+        const int64_t k = back ? count - 1 - c : c, len = min(seg, n - k * seg);
+        const int64_t to = ((first + k) * d.nheads + h) * PN + at;
+        f32x4 add = {0.f, 0.f, 0.f, 0.f}, dadd = {0.f, 0.f, 0.f, 0.f};
+        if (c + 1 < count) {                                       // (nothing is left there for the last)
+            add = *reinterpret_cast<const f32x4*>(loc + to);
+            if constexpr (kDg) dadd = *reinterpret_cast<const f32x4*>(dloc + to);
+        }
+        *reinterpret_cast<f32x4*>(loc + to) = s;
+        if constexpr (kDg) *reinterpret_cast<f32x4*>(dloc + to) = ds;
+        const float grow = expm1f(gl * (float)len);
+#pragma unroll
+        for (int m = 0; m < 4; ++m) {
+            if constexpr (kDg) {
+                const float both = fmaf((float)len, s[m], ds[m]);
+                ds[m] = fmaf(both, grow, both) + dadd[m];
+            }
+            s[m] = fmaf(s[m], grow, s[m]) + add[m];
+        }
+    }
+}
+
+// dg of a head: the walks' sums in a fixed order, in 64 bits.
+__global__ __launch_bounds__(256) void linear_dg_kernel(const float* __restrict__ part, float* __restrict__ dg,
+                                                        int64_t items, int64_t nheads, int parts)
+{
+    __shared__ double sums[256];
+    const int64_t h = blockIdx.x;
+    double s = 0.0;
+    for (int64_t i = threadIdx.x; i < items * parts; i += 256) s += part[((i / parts) * nheads + h) * parts + i % parts];
+    sums[threadIdx.x] = s;
+    __syncthreads();
+    for (int n = 128; n > 0; n >>= 1) {
+        if ((int)threadIdx.x < n) sums[threadIdx.x] += sums[threadIdx.x + n];
+        __syncthreads();
+    }
+    if (threadIdx.x == 0) dg[h] = (float)sums[0];
+}
+
+// The gradient of a shared key or value: the sum of its heads' in their order, rounded once.
+template <typename T>
+__global__ __launch_bounds__(256) void linear_group_kernel(const float* __restrict__ part, T* __restrict__ out,
+                                                           int64_t rows, int share, int width)
+{
+    const int64_t quads = width / 4;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= rows * quads) return;
+    const int64_t row = i / quads, at = 4 * (i % quads);
+    const float* from = part + row * share * width + at;
+    f32x4 s = *reinterpret_cast<const f32x4*>(from);
+    for (int m = 1; m < share; ++m) s += *reinterpret_cast<const f32x4*>(from + (int64_t)m * width);
+    store4(out + row * width + at, s[0], s[1], s[2], s[3]);
+}
+
+unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); }
+
+size_t bytes_up(int64_t floats) { return ((size_t)floats * 4 + 255) / 256 * 256; }
+
+// Tokens of a segment.  A walk takes one workgroup; two fit a CU.
+int64_t linear_segment(const DeltaDims& d, int64_t slices)
+{
+    constexpr int64_t kCUs = 256, kLeast = 256;
+    const int64_t walks = d.seqs * d.nheads * slices;
+    int64_t seg;
+    if (d.cu) {
+        seg = std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
+    } else {
+        if (walks == 0 || walks >= kCUs) return kWholeRows;
+        const int64_t n = std::min<int64_t>(2 * kCUs / walks, d.seqlen / kLeast);
+        if (n <= 1) return kWholeRows;
+        seg = (d.seqlen + n - 1) / n;
+    }
+    seg = (seg + 63) / 64 * 64;
+    return (d.cu ? d.tokens : d.seqlen) <= seg ? kWholeRows : seg;
+}
+
+int64_t forward_segment(const DeltaDims& d, int elem_bytes)
+{
+    const int columns = linear_columns(elem_bytes, false, (int)d.headdim);
+    return linear_segment(d, (d.headdim + columns - 1) / columns);
+}
+
+int64_t state_floats(const DeltaDims& d, int64_t items) { return items * d.nheads * d.headdim * d.dstate; }
+
+// The walk, or where rows are cut its three steps; states: room for the items' states (kDg: twice that).
+template <typename T, bool kDg>
+hipError_t walk(LinearWalk<T> p, const float* enter, float* states, hipStream_t stream)
+{
+    const bool cut = p.seg != kWholeRows;
+    p.enter = enter;
+    p.denter = nullptr;
+    p.by_item = false;
+    if (cut) {
+        const int64_t PN = p.d.headdim * p.d.dstate;
+        LinearWalk<T> first = p;
+        first.fin = states;
+        first.dfin = kDg ? states + bytes_up(state_floats(p.d, linear_items(p.d, p.seg))) / 4 : nullptr;
+        hipError_t e = launch_linear_walk<T, false, kDg>(first, stream);
+        if (e != hipSuccess) return e;
+        hipLaunchKernelGGL((linear_join_kernel<kDg>), dim3(blocks_of(p.d.seqs * p.d.nheads * PN / 4)), dim3(256), 0, stream,
+                           first.fin, first.dfin, enter, p.g, p.d, p.seg, p.back, PN);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        p.enter = first.fin;
+        p.denter = first.dfin;
+        p.by_item = true;
+    }
+    return launch_linear_walk<T, true, kDg>(p, stream);
+}
+
+struct GradLayout {
+    int64_t seg, items;
+    int parts;
+    size_t states, dpart, dk, dv, total;
+};
+
+GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
+{
+    GradLayout l;
+    // the same segments for all three walks, by the one with the fewest workgroups
+    const int64_t most = std::max<int64_t>(linear_columns(elem_bytes, false, (int)d.headdim),
+                                           linear_columns(elem_bytes, true, (int)d.dstate));
+    l.seg = linear_segment(d, std::max<int64_t>(1, std::min(d.headdim, d.dstate) / most));
+    l.items = linear_items(d, l.seg);
+    const int columns = linear_columns(elem_bytes, true, (int)d.dstate);
+    l.parts = (int)((d.dstate + columns - 1) / columns) * linear_waves(elem_bytes, true, (int)d.dstate);
+    l.states = 0;
+    l.dpart = l.states + (l.seg == kWholeRows ? 0 : 2 * bytes_up(state_floats(d, l.items)));
+    l.dk = l.dpart + bytes_up(l.items * d.nheads * l.parts);
+    const bool shared = d.nheads != d.ngroups;
+    l.dv = l.dk + (shared ? bytes_up(d.tokens * d.nheads * d.dstate) : 0);
+    l.total = l.dv + (shared ? bytes_up(d.tokens * d.nheads * d.headdim) : 0) + 256;
+    return l;
+}
+
+}  // namespace
+
+size_t linear_forward_workspace(const DeltaDims& d, int elem_bytes)
+{
+    const int64_t seg = forward_segment(d, elem_bytes);
+    return 256 + (seg == kWholeRows ? 0 : bytes_up(state_floats(d, linear_items(d, seg))));
+}
+
+size_t linear_backward_workspace(const DeltaDims& d, int elem_bytes) { return grad_layout(d, elem_bytes).total; }
+
+int64_t linear_blocks(const DeltaDims& d, int elem_bytes)
+{
+    const int64_t seg = std::min(forward_segment(d, elem_bytes), grad_layout(d, elem_bytes).seg);
+    return linear_items(d, seg) * d.nheads * ((std::max(d.headdim, d.dstate) + 63) / 64);
+}
+
+template <typename T>
+hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T* q, const float* init, T* y,
+                                 float* fin, const DeltaDims& d, void* workspace, hipStream_t stream)
+{
+    const int share = (int)(d.nheads / d.ngroups);
+    LinearWalk<T> p{};
+    p.q = {q, d.nheads * d.dstate, 1};
+    p.k = {k, d.ngroups * d.dstate, share};
+    p.v = {v, d.ngroups * d.headdim, share};
+    p.o = y;
+    p.g = g;
+    p.fin = fin;
+    p.sk = 1;
+    p.sv = d.dstate;
+    p.Dk = (int)d.dstate;
+    p.Dv = (int)d.headdim;
+    p.d = d;
+    p.seg = forward_segment(d, sizeof(T));
+    return walk<T, false>(p, init, static_cast<float*>(workspace), stream);
+}
+
+template <typename T>
+hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const T* q, const float* init, const T* dy,
+                                  const float* dfinal, T* dv, float* dg, T* dk, T* dq, float* dinit, const DeltaDims& d,
+                                  void* workspace, hipStream_t stream)
+{
+    const GradLayout l = grad_layout(d, sizeof(T));
+    char* ws = static_cast<char*>(workspace);
+    float* states = reinterpret_cast<float*>(ws + l.states);
+    float* dpart = reinterpret_cast<float*>(ws + l.dpart);
+    const int share = (int)(d.nheads / d.ngroups);
+    const bool shared = share > 1;
+    const LinearOperand<T> oq = {q, d.nheads * d.dstate, 1}, ok = {k, d.ngroups * d.dstate, share},
+                           ov = {v, d.ngroups * d.headdim, share}, od = {dy, d.nheads * d.headdim, 1};
+    LinearWalk<T> p{};
+    p.g = g;
+    p.d = d;
+    p.seg = l.seg;
+    // dq: the rows of the walk's state are the state's rows, its columns the columns
+    p.q = od;
+    p.k = ov;
+    p.v = ok;
+    p.x = oq;
+    p.o = dq;
+    p.sk = d.dstate;
+    p.sv = 1;
+    p.Dk = (int)d.headdim;
+    p.Dv = (int)d.dstate;
+    p.dlast = dfinal;
+    p.dpart = dpart;
+    hipError_t e = walk<T, true>(p, init, states, stream);
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(linear_dg_kernel, dim3((unsigned)d.nheads), dim3(256), 0, stream, dpart, dg, l.items, d.nheads,
+                       l.parts);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+    // dk
+    p.q = ov;
+    p.k = od;
+    p.v = oq;
+    p.x = {};
+    p.dlast = nullptr;
+    p.dpart = nullptr;
+    p.back = true;
+    p.of32 = shared;
+    p.o = shared ? static_cast<void*>(ws + l.dk) : dk;
+    if ((e = walk<T, false>(p, dfinal, states, stream)) != hipSuccess) return e;
+    // dv, and the gradient of the state before the first token
+    p.q = ok;
+    p.k = oq;
+    p.v = od;
+    p.o = shared ? static_cast<void*>(ws + l.dv) : dv;
+    p.sk = 1;
+    p.sv = d.dstate;
+    p.Dk = (int)d.dstate;
+    p.Dv = (int)d.headdim;
+    p.fin = dinit;
+    if ((e = walk<T, false>(p, dfinal, states, stream)) != hipSuccess) return e;
+    if (shared && d.tokens > 0) {
+        const int64_t rows = d.tokens * d.ngroups;
+        hipLaunchKernelGGL((linear_group_kernel<T>), dim3(blocks_of(rows * d.dstate / 4)), dim3(256), 0, stream,
+                           reinterpret_cast<const float*>(ws + l.dk), dk, rows, share, (int)d.dstate);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+        hipLaunchKernelGGL((linear_group_kernel<T>), dim3(blocks_of(rows * d.headdim / 4)), dim3(256), 0, stream,
+                           reinterpret_cast<const float*>(ws + l.dv), dv, rows, share, (int)d.headdim);
+        e = hipGetLastError();
+    }
+    return e;
+}
+
+#define SSD_LINEAR(T)                                                                                                  \
+    template hipError_t launch_linear_forward<T>(const T*, const float*, const T*, const T*, const float*, T*, float*,  \
+                                                 const DeltaDims&, void*, hipStream_t);                                \
+    template hipError_t launch_linear_backward<T>(const T*, const float*, const T*, const T*, const float*, const T*,  \
+                                                  const float*, T*, float*, T*, T*, float*, const DeltaDims&, void*,   \
+                                                  hipStream_t);
+SSD_LINEAR(float)
+SSD_LINEAR(bf16)
+#undef SSD_LINEAR
+
+}  // namespace ssd

@@ -92,6 +92,22 @@ def load_library():
     lib.ssd_delta_backward.argtypes = [vp] * 14 + [i64] * 6 + [i32, vp, sz, vp]
     lib.ssd_delta_step.restype = i32
     lib.ssd_delta_step.argtypes = [vp] * 7 + [i64] * 5 + [i32, vp]
+    lib.ssd_linear_forward_workspace_bytes.restype = sz
+    lib.ssd_linear_forward_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_linear_forward.restype = i32
+    lib.ssd_linear_forward.argtypes = [vp] * 7 + [i64] * 6 + [i32, vp, sz, vp]
+    lib.ssd_linear_forward_varlen_workspace_bytes.restype = sz
+    lib.ssd_linear_forward_varlen_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_linear_forward_varlen.restype = i32
+    lib.ssd_linear_forward_varlen.argtypes = [vp] * 5 + [i64] + [vp] * 3 + [i64] * 5 + [i32, vp, sz, vp]
+    lib.ssd_linear_backward_workspace_bytes.restype = sz
+    lib.ssd_linear_backward_workspace_bytes.argtypes = [i64] * 6 + [i32]
+    lib.ssd_linear_backward.restype = i32
+    lib.ssd_linear_backward.argtypes = [vp] * 12 + [i64] * 6 + [i32, vp, sz, vp]
+    lib.ssd_linear_step.restype = i32
+    lib.ssd_linear_step.argtypes = [vp] * 2 + [i64] + [vp] * 5 + [i64] * 5 + [i32, vp]
+    lib.ssd_state_move.restype = i32
+    lib.ssd_state_move.argtypes = [vp] * 3 + [i64] * 4 + [vp]
     _lib = lib
     return lib
 
@@ -512,6 +528,171 @@ def delta_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torc
                                 code, _stream(dev))
     _check("ssd_delta_step", rc)
     return y
+
+
+# --- linear attention with a decay for each head, and pools of states --------------------------
+
+def _linear_need(v, g, k, q, lead, H, P, N, G, dev):
+    _need(v, "v", (*lead, G, P), v.dtype, dev)
+    _need(g, "g", (H,), torch.float32, dev)
+    _need(k, "k", (*lead, G, N), v.dtype, dev)
+    _need(q, "q", (*lead, H, N), v.dtype, dev)
+
+
+def linear_forward(v: torch.Tensor, g: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+                   init_states: Optional[torch.Tensor] = None,
+                   workspace: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Linear attention with a decay for each head over whole sequences: returns (y, final_states); see ssd_linear_forward.
+
+    v (batch, seqlen, ngroups, headdim) in bf16 or fp32; g (nheads,) fp32, the log decays; k (batch, seqlen, ngroups,
+    dstate) and q (batch, seqlen, nheads, dstate) in v's dtype; init_states (batch, nheads, headdim, dstate) fp32 or
+    None.  A workspace (uint8, ssd_linear_forward_workspace_bytes() long) may be passed in."""
+    lib = load_library()
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, ngroups, headdim) and q (batch, seqlen, nheads, dstate)")
+    b, L, G, P = v.shape
+    H, N = q.shape[2], q.shape[3]
+    dev = v.device
+    code = _dtype_code(v)
+    _linear_need(v, g, k, q, (b, L), H, P, N, G, dev)
+    if init_states is not None:
+        _need(init_states, "init_states", (b, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_linear_forward_workspace_bytes(b, L, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_linear_forward_workspace_bytes", -2)
+    if workspace is None:
+        workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    else:
+        _need(workspace, "workspace", (workspace.numel(),), torch.uint8, dev)
+    y = torch.empty((b, L, H, P), dtype=v.dtype, device=dev)
+    final = torch.empty((b, H, P, N), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        rc = lib.ssd_linear_forward(_ptr(v), _ptr(g), _ptr(k), _ptr(q), _ptr(init_states), _ptr(y), _ptr(final), b, L,
+                                    H, P, N, G, code, _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("ssd_linear_forward", rc)
+    return y, final
+
+
+def linear_forward_varlen(v: torch.Tensor, g: torch.Tensor, k: torch.Tensor, q: torch.Tensor, cu_seqlens: torch.Tensor,
+                          init_states: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """Packed variable-length batch of linear attention; see ssd_linear_forward_varlen.
+
+    v (T, ngroups, headdim); g (nheads,) fp32; k (T, ngroups, dstate), q (T, nheads, dstate) in v's dtype; cu_seqlens
+    int32 (nseq + 1,) on the same device; init_states (nseq, nheads, headdim, dstate) fp32 or None.
+    Returns (y (T, nheads, headdim) in v's dtype, final_states (nseq, nheads, headdim, dstate))."""
+    lib = load_library()
+    if v.dim() != 3 or q.dim() != 3:
+        raise ValueError("v must be (T, ngroups, headdim) and q (T, nheads, dstate)")
+    T, G, P = v.shape
+    H, N = q.shape[1], q.shape[2]
+    dev = v.device
+    code = _dtype_code(v)
+    _linear_need(v, g, k, q, (T,), H, P, N, G, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must be a 1-D tensor of nseq + 1 offsets")
+    _need(cu_seqlens, "cu_seqlens", (cu_seqlens.numel(),), torch.int32, dev)
+    nseq = cu_seqlens.numel() - 1
+    if init_states is not None:
+        _need(init_states, "init_states", (nseq, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_linear_forward_varlen_workspace_bytes(T, nseq, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_linear_forward_varlen_workspace_bytes", -2)
+    workspace = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    y = torch.empty((T, H, P), dtype=v.dtype, device=dev)
+    final = torch.empty((nseq, H, P, N), dtype=torch.float32, device=dev)
+    with _on_device(dev):
+        rc = lib.ssd_linear_forward_varlen(_ptr(v), _ptr(g), _ptr(k), _ptr(q), _ptr(cu_seqlens), nseq,
+                                           _ptr(init_states), _ptr(y), _ptr(final), T, H, P, N, G, code,
+                                           _ptr(workspace), workspace.numel(), _stream(dev))
+    _check("ssd_linear_forward_varlen", rc)
+    return y, final
+
+
+def linear_backward(v: torch.Tensor, g: torch.Tensor, k: torch.Tensor, q: torch.Tensor, dy: torch.Tensor,
+                    init_states: Optional[torch.Tensor] = None, dfinal: Optional[torch.Tensor] = None) -> dict:
+    """Gradients of ``linear_forward`` for dL/dy = dy and dL/d(final_states) = dfinal (None = 0); see
+    ssd_linear_backward.  Returns a dict with dv, dg, dk, dq, dinit (dv, dk, dq in v's dtype)."""
+    lib = load_library()
+    if v.dim() != 4 or q.dim() != 4:
+        raise ValueError("v must be (batch, seqlen, ngroups, headdim) and q (batch, seqlen, nheads, dstate)")
+    b, L, G, P = v.shape
+    H, N = q.shape[2], q.shape[3]
+    dev = v.device
+    code = _dtype_code(v)
+    _linear_need(v, g, k, q, (b, L), H, P, N, G, dev)
+    _need(dy, "dy", (b, L, H, P), v.dtype, dev)
+    if init_states is not None:
+        _need(init_states, "init_states", (b, H, P, N), torch.float32, dev)
+    if dfinal is not None:
+        _need(dfinal, "dfinal", (b, H, P, N), torch.float32, dev)
+    ws_bytes = lib.ssd_linear_backward_workspace_bytes(b, L, H, P, N, G, code)
+    if ws_bytes == 0:
+        raise SSDError("ssd_linear_backward_workspace_bytes", -2)
+    ws = torch.empty(ws_bytes, dtype=torch.uint8, device=dev)
+    out = dict(dv=torch.empty_like(v), dg=torch.empty_like(g), dk=torch.empty_like(k), dq=torch.empty_like(q),
+               dinit=torch.empty((b, H, P, N), dtype=torch.float32, device=dev))
+    with _on_device(dev):
+        rc = lib.ssd_linear_backward(_ptr(v), _ptr(g), _ptr(k), _ptr(q), _ptr(init_states), _ptr(dy), _ptr(dfinal),
+                                     _ptr(out["dv"]), _ptr(out["dg"]), _ptr(out["dk"]), _ptr(out["dq"]),
+                                     _ptr(out["dinit"]), b, L, H, P, N, G, code, _ptr(ws), ws.numel(), _stream(dev))
+    _check("ssd_linear_backward", rc)
+    return out
+
+
+def linear_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, k: torch.Tensor, q: torch.Tensor,
+                slots: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """One token of linear attention: advances ``state`` in place and returns y; see ssd_linear_step.
+
+    state (nslots, nheads, headdim, dstate) fp32; v (batch, ngroups, headdim) in bf16 or fp32; g (nheads,) fp32; k
+    (batch, ngroups, dstate) and q (batch, nheads, dstate) in v's dtype.  slots int32 (batch,): row i advances
+    state[slots[i]], a row with a slot out of range (-1) none, and its y is zero; None: nslots = batch, row i has state[i]."""
+    lib = load_library()
+    if state.dim() != 4 or v.dim() != 3:
+        raise ValueError("state must be (nslots, nheads, headdim, dstate) and v (batch, ngroups, headdim)")
+    n, H, P, N = state.shape
+    b, G = v.shape[0], v.shape[1]
+    dev = state.device
+    code = _dtype_code(v)
+    _need(state, "state", (b if slots is None else n, H, P, N), torch.float32, dev)
+    _linear_need(v, g, k, q, (b,), H, P, N, G, dev)
+    if slots is not None:
+        _need(slots, "slots", (b,), torch.int32, dev)
+    if y is None:
+        y = torch.empty((b, H, P), dtype=v.dtype, device=dev)
+    else:
+        _need(y, "y", (b, H, P), v.dtype, dev)
+    with _on_device(dev):
+        rc = lib.ssd_linear_step(_ptr(state), _ptr(slots), n, _ptr(v), _ptr(g), _ptr(k), _ptr(q), _ptr(y), b, H, P, N,
+                                 G, code, _stream(dev))
+    _check("ssd_linear_step", rc)
+    return y
+
+
+def state_move(states: torch.Tensor, src: torch.Tensor, source: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Copies, forks, reorders, compacts or frees the states of a pool by one map of slots; see ssd_state_move.
+
+    states (nslots, nheads, headdim, dstate) or (nlayers, nslots, nheads, headdim, dstate) fp32, changed in place and
+    returned; src int32 (nslots,): slot i becomes source[src[i]], zeros where src[i] is -1, and stays otherwise.  source:
+    another pool of the same layers and state sizes, or None: the pool itself, as it was before the call."""
+    lib = load_library()
+    if states.dim() not in (4, 5):
+        raise ValueError("states must be ([nlayers,] nslots, nheads, headdim, dstate)")
+    lead, n, one = states.shape[:-4], states.shape[-4], states.shape[-3:]
+    dev = states.device
+    _need(states, "states", states.shape, torch.float32, dev)
+    _need(src, "src", (n,), torch.int32, dev)
+    m = n
+    if source is not None:
+        if source.dim() != states.dim():
+            raise ValueError("source must have as many dimensions as states")
+        m = source.shape[-4]
+        _need(source, "source", (*lead, m, *one), torch.float32, dev)
+    layers = lead[0] if lead else 1
+    with _on_device(dev):
+        rc = lib.ssd_state_move(_ptr(states), _ptr(source), _ptr(src), layers, n, m, one[0] * one[1] * one[2],
+                                _stream(dev))
+    _check("ssd_state_move", rc)
+    return states
 
 
 # --- the four stages of the chunked mode, one entry point each ---------------------------------
