@@ -22,10 +22,11 @@
 // where X is what dL/dO is contracted with: for dq = (dy, v, k) X is q.  No difference of large sums is formed.
 //
 // Columns of the state do not mix: a wavefront keeps JT x 16 of them for the whole walk as accumulator tiles (rows Dk,
-// columns Dv), which are operand fragments as they are (see common.hpp).  It works out all scores of a chunk by itself:
-// the K and Q fragments are read for the state's products in any case, and in return the wavefronts exchange nothing and
-// a chunk has one barrier, behind the copies.  Two stages of LDS: a chunk's copies run while the one before it is
-// worked on.
+// columns Dv), which are operand fragments as they are (see common.hpp).  The chunk's scores are needed by all of them:
+// three make a 16 x 16 tile each, one chunk ahead of the one whose state products run, so that a chunk has one barrier.
+// Copies run two to four stages of LDS ahead.  (Fewer stages, where the rows are wide: the scores are made in their own
+// chunk, with a second barrier.)  Chunks have 32 tokens: with 64 the scores are more than what is saved per
+// chunk, and the registers do not hold what is read ahead.
 //
 // A row may be cut into segments that walk at the same time: a first pass of the same kernel (states only) leaves
 // what each adds to the state, linear_join carries the states over, and the walk starts each segment from its own.
@@ -172,50 +173,141 @@ struct LinearCopy {
 
 // ---- the walk -------------------------------------------------------------------------------------------
 
-template <typename T, int KB, int NW, int JT, int C, bool kOut, bool kDg> struct LinearShape {
+constexpr int kLC = 32;      // tokens of a chunk
+
+template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg> struct LinearShape {
     static constexpr int kEs = (int)sizeof(T);
     static constexpr int CHk = KB * 32 * kEs / 16, CHv = NW * JT * 16 * kEs / 16;
-    static constexpr int kSB = C / 32;
-    static constexpr int kQK = 32 * CHk * 16, kV = 32 * CHv * 16;     // bytes of a tile of 32 rows
-    static constexpr int kAtK = kOut ? kSB * kQK : 0;
-    static constexpr int kAtV = kAtK + kSB * kQK;
-    static constexpr int kAtX = kAtV + kSB * kV;
-    static constexpr int kStage = kAtX + (kOut && kDg ? kSB * kV : 0);
+    static constexpr int kQK = kLC * CHk * 16, kV = kLC * CHv * 16;   // bytes of a tile
+    static constexpr int kAtK = kOut ? kQK : 0;
+    static constexpr int kAtV = kAtK + kQK;
+    static constexpr int kAtX = kAtV + kV;
+    // (two stages of the widest fp32 rows leave no room for X: it is read from memory)
+    static constexpr bool kHasX = kOut && kDg && !(kEs == 4 && KB == 8);
+    static constexpr int kStage = kAtX + (kHasX ? kV : 0);
+    // three 16 x 16 tiles of decayed scores as operand quads
+    static constexpr int kScores = kOut ? 3 * 64 * 4 * kEs : 0;
+    static constexpr int kFit = (kBudget - 2 * kScores) / kStage;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr bool kPipe = kOut && kStages > 2;                // a chunk's scores are made while the one before is read
+    static constexpr int kLds = kStages * kStage + (kPipe ? 2 : 1) * kScores;
+    // what every wavefront issues at least: copies for a chunk, stores of a chunk's outputs
+    static constexpr int kCopies = (kOut ? 2 : 1) * (DTile<CHk>::kInst / NW) + (kHasX ? 2 : 1) * (DTile<CHv>::kInst / NW);
+    static constexpr int kStores = kOut ? 2 * JT : 0;
+    // wavefronts a SIMD that the registers are shared out for: two, unless the states alone take half of what they would have
+    static constexpr int kWaves = KB * 8 * JT * (kDg ? 2 : 1) <= (sizeof(T) == 2 ? 127 : 63) ? 2 : 1;
 };
 
-// A DTile's fragment along row 16 t + r (the slots of DRows), for a block of 32 elements that is not a constant.
-template <typename T, int CH>
-__device__ __forceinline__ void linear_rows_any(Vec8<T>& f, unsigned tile, int t, int kb, int r, int g)
-{
+// Operand fragments of a stage.  What changes with the stage is added to the lane's addresses once a chunk (at), the
+// rest are constants.
+template <typename T, int CH> struct LinearRows;
+template <int CH> struct LinearRows<bf16, CH> {
+    static constexpr int kPer = DRows<bf16, CH>::kPer;
+    const DRows<bf16, CH> d;
+    unsigned b[2][kPer][2];
+    __device__ __forceinline__ LinearRows(int r, int g) : d(r, g) {}
+    // (rows 16 on have addresses of their own: from one, the compiler would read both rows' quads in one instruction, and
+    // move them to their fragments after)
+    __device__ __forceinline__ void at(unsigned stage)
+    {
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-        const int byte = (32 * kb + 16 * x + 4 * g) * (int)sizeof(T);
-        const unsigned at = tile + DTile<CH>::offset(16 * t + r, byte >> 4) + (byte & 15);
-        if constexpr (sizeof(T) == 2) {
-            const bf16x4 q = lds_at<bf16x4>(at);
+        for (int k = 0; k < kPer; ++k)
 #pragma unroll
-            for (int m = 0; m < 4; ++m) f.v[4 * x + m] = q[m];
-        } else {
-            const f32x4 q = lds_at<f32x4>(at);
-#pragma unroll
-            for (int m = 0; m < 4; ++m) f.v[4 * x + m] = q[m];
-        }
+            for (int x = 0; x < 2; ++x) {
+                b[0][k][x] = b[1][k][x] = d.a[k][x] + stage;
+                asm("" : "+v"(b[1][k][x]));
+            }
     }
-}
+    // row 16 t + r of the tile `tile` bytes into the stage, block kb of 32 elements
+    __device__ __forceinline__ void load(Vec8<bf16>& f, int tile, int t, int kb) const
+    {
+        const int o = tile + t * (16 * CH * 16) + (kb / kPer) * 256;
+        const bf16x4 x = lds_at<bf16x4>(b[t][kb % kPer][0] + o), y = lds_at<bf16x4>(b[t][kb % kPer][1] + o);
+        f.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+    }
+};
+template <int CH> struct LinearRows<float, CH> {
+    const DRows<float, CH> d;
+    unsigned stage;
+    __device__ __forceinline__ LinearRows(int r, int g) : d(r, g) {}
+    __device__ __forceinline__ void at(unsigned s) { stage = s; }
+    __device__ __forceinline__ void load(Vec8<float>& f, int tile, int t, int kb) const { d.load(f, stage + tile, t, kb); }
+};
+template <typename T, int CH> struct LinearCols;
+template <int CH> struct LinearCols<bf16, CH> {
+    static constexpr int kPer = DCols<bf16, CH>::kPer;
+    const DCols<bf16, CH> d;
+    unsigned b[kPer];
+    __device__ __forceinline__ LinearCols(int r, int g) : d(r, g) {}
+    __device__ __forceinline__ void at(unsigned stage)
+    {
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) b[k] = d.a[k] + stage;
+    }
+    __device__ __forceinline__ void load(Vec8<bf16>& f, int tile, int t) const
+    {
+        typedef short v4i16 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) v4i16* P;
+        const unsigned o = b[t % kPer] + (tile + (t / kPer) * 256);
+        const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(uintptr_t)o);
+        const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(uintptr_t)(o + 16 * CH * 16));
+        f.v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+};
+template <int CH> struct LinearCols<float, CH> {
+    const DCols<float, CH> d;
+    unsigned stage;
+    __device__ __forceinline__ LinearCols(int r, int g) : d(r, g) {}
+    __device__ __forceinline__ void at(unsigned s) { stage = s; }
+    __device__ __forceinline__ void load(Vec8<float>& f, int tile, int t) const { d.load(f, stage + tile, t); }
+};
 
-// the 4 values of a T quad at an LDS address as floats
+// the 4 values of a T quad at an LDS address, as floats
 __device__ __forceinline__ f32x4 lds_quad(unsigned a, bf16)
 {
     const bf16x4 q = lds_at<bf16x4>(a);
     return f32x4{(float)q[0], (float)q[1], (float)q[2], (float)q[3]};
 }
 __device__ __forceinline__ f32x4 lds_quad(unsigned a, float) { return lds_at<f32x4>(a); }
-
-template <typename T, int KB, int NW, int JT, int C, bool kOut, bool kDg>
-__global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
+// and put there
+__device__ __forceinline__ void lds_put(unsigned a, const f32x4& v, bf16)
 {
-    using S = LinearShape<T, KB, NW, JT, C, kOut, kDg>;
-    constexpr int CHk = S::CHk, CHv = S::CHv, kSB = S::kSB, kTT = C / 16, kNT = 2 * KB;
+    *(__attribute__((address_space(3))) u32x2*)(uintptr_t)a = __builtin_bit_cast(u32x2, pack4_bf16(v));
+}
+__device__ __forceinline__ void lds_put(unsigned a, const f32x4& v, float)
+{
+    *(__attribute__((address_space(3))) f32x4*)(uintptr_t)a = v;
+}
+// a fragment of two quads side by side, and one with zeros in its upper half
+__device__ __forceinline__ void lds_frag(Vec8<bf16>& f, unsigned a) { f.v = lds_at<bf16x8>(a); }
+__device__ __forceinline__ void lds_frag(Vec8<float>& f, unsigned a)
+{
+    const f32x4 x = lds_at<f32x4>(a), y = lds_at<f32x4>(a + 16);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) { f.v[m] = x[m]; f.v[4 + m] = y[m]; }
+}
+__device__ __forceinline__ void lds_half(Vec8<bf16>& f, unsigned a)
+{
+    f.zero();
+    const bf16x4 q = lds_at<bf16x4>(a);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) f.v[m] = q[m];
+}
+__device__ __forceinline__ void lds_half(Vec8<float>& f, unsigned a)
+{
+    const f32x4 x = lds_at<f32x4>(a);
+#pragma unroll
+    for (int m = 0; m < 4; ++m) { f.v[m] = x[m]; f.v[4 + m] = 0.f; }
+}
+
+template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(
+    LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves, LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves)))
+void linear_walk_kernel(LinearWalk<T> p)
+{
+    using S = LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>;
+    constexpr int CHk = S::CHk, CHv = S::CHv, kNT = 2 * KB, kStages = S::kStages;
+    static_assert(NW >= 3, "three wavefronts make a chunk's scores");
     extern __shared__ __attribute__((aligned(1024))) unsigned char lds_raw[];
     const unsigned lds = lds_addr(lds_raw);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id();
@@ -237,72 +329,70 @@ __global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
     const int validk = p.Dk * S::kEs / 16, validv = min(CHv, (p.Dv - col0) * S::kEs / 16);
     const float gl = fmaxf(p.g[h], -1000.f);
 
-    // sources: head's first column, the walk's first token
+    // sources: the head's first column, the walk's first token; from there 32 tokens on with every chunk
     const char* src[4];
-    unsigned row_bytes[4];
-    {
-        const LinearOperand<T>* ops[4] = {&p.q, &p.k, &p.v, &p.x};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int width = i < 2 ? p.Dk : p.Dv;
-            row_bytes[i] = (unsigned)(ops[i]->row * S::kEs);
-            const int64_t tok = p.back ? it.start + it.len - 32 : it.start;
-            src[i] = (const char*)ops[i]->p + tok * (int64_t)row_bytes[i] +
-                     ((int64_t)(h / max(ops[i]->share, 1)) * width + (i < 2 ? 0 : col0)) * S::kEs;
-        }
-    }
+    int64_t step[4];
     LinearCopy<CHk, NW> copyq, copyk;
     LinearCopy<CHv, NW> copyv, copyx;
-    if constexpr (kOut) copyq.plan(row_bytes[0], p.back, wave, lane);
-    copyk.plan(row_bytes[1], p.back, wave, lane);
-    copyv.plan(row_bytes[2], p.back, wave, lane);
-    if constexpr (kOut && kDg) copyx.plan(row_bytes[3], p.back, wave, lane);
-
-    auto issue = [&](int c, unsigned stage) {
+    {
+        const LinearOperand<T>* ops[4] = {&p.q, &p.k, &p.v, &p.x};
+        unsigned row_bytes[4];
 #pragma unroll
-        for (int sb = 0; sb < kSB; ++sb) {
-            const int t0 = c * C + 32 * sb, rows = it.len - t0;
-            const int64_t step = p.back ? -(int64_t)t0 : (int64_t)t0;
-            if constexpr (kOut) copyq.issue(src[0] + step * row_bytes[0], rows, validk, stage + sb * S::kQK, wave, lane);
-            copyk.issue(src[1] + step * row_bytes[1], rows, validk, stage + S::kAtK + sb * S::kQK, wave, lane);
-            copyv.issue(src[2] + step * row_bytes[2], rows, validv, stage + S::kAtV + sb * S::kV, wave, lane);
-            if constexpr (kOut && kDg)
-                copyx.issue(src[3] + step * row_bytes[3], rows, validv, stage + S::kAtX + sb * S::kV, wave, lane);
+        for (int i = 0; i < 4; ++i) {
+            row_bytes[i] = (unsigned)(ops[i]->row * S::kEs);
+            step[i] = p.back ? -(int64_t)kLC * row_bytes[i] : (int64_t)kLC * row_bytes[i];
+            const int64_t tok = p.back ? it.start + it.len - kLC : it.start;
+            src[i] = (const char*)ops[i]->p + tok * (int64_t)row_bytes[i] +
+                     ((int64_t)(h / max(ops[i]->share, 1)) * (i < 2 ? p.Dk : p.Dv) + (i < 2 ? 0 : col0)) * S::kEs;
         }
+        if constexpr (kOut) copyq.plan(row_bytes[0], p.back, wave, lane);
+        copyk.plan(row_bytes[1], p.back, wave, lane);
+        copyv.plan(row_bytes[2], p.back, wave, lane);
+        if constexpr (S::kHasX) copyx.plan(row_bytes[3], p.back, wave, lane);
+    }
+    [[maybe_unused]] const char* xrows = src[3];                  // X of the chunk, where it is not in LDS
+    int left = it.len;
+    auto issue = [&](unsigned stage) {
+        if constexpr (kOut) copyq.issue(src[0], left, validk, stage, wave, lane);
+        copyk.issue(src[1], left, validk, stage + S::kAtK, wave, lane);
+        copyv.issue(src[2], left, validv, stage + S::kAtV, wave, lane);
+        if constexpr (S::kHasX) copyx.issue(src[3], left, validv, stage + S::kAtX, wave, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] += step[i];
+        left -= kLC;
     };
 
     if (validk < CHk || validv < CHv) {
         // columns that no copy writes hold zeros
-        for (int i = threadIdx.x * 16; i < 2 * S::kStage; i += NW * 64 * 16)
+        for (int i = threadIdx.x * 16; i < kStages * S::kStage; i += NW * 64 * 16)
             *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(lds + i) = u32x4{0, 0, 0, 0};
         __syncthreads();
     }
-    const int nchunks = (it.len + C - 1) / C;
-    if (nchunks > 0) issue(0, lds);
+    const int nchunks = (it.len + kLC - 1) / kLC;
+    for (int c = 0; c < kStages - 1 && c < nchunks; ++c) issue(lds + c * S::kStage);
 
     // ---- tables of powers
     const int e = p.back ? 0 : 1;
-    float diag[4], off[4], outw[kSB][8];
+    const float a16 = expf(gl * 16.f);
+    const float into0 = expf(gl * (r + e)), into1 = into0 * a16;  // a^(t + e)
+    // the tile of scores that this wavefront makes: t, s = (0, 0), (1, 0), (1, 1); its weights, and t - s times those
+    const int tile_t = wave > 0, tile_s = wave == 2;
+    float tilew[4];
+    [[maybe_unused]] float tiled[4];
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
-        const int gap = r - 4 * g4 - m;                           // t - s within a 16 x 16 tile
-        diag[m] = gap >= 0 ? expf(gl * gap) : 0.f;
-        off[m] = expf(gl * (16 + gap));
+        const int gap = 16 * (tile_t - tile_s) + r - 4 * g4 - m;
+        tilew[m] = gap >= 0 ? expf(gl * gap) : 0.f;
+        tiled[m] = gap > 0 ? tilew[m] * gap : 0.f;
     }
-    const float a16 = expf(gl * 16.f);
-    const float into = expf(gl * (r + e));
-    float grow;                                                   // a^C - 1: the state's own share stays exact
+    float outw[8];
+    float grow;                                                   // a^32 - 1: the state's own share stays exact
     auto weights = [&](int rows) {
 #pragma unroll
-        for (int sb = 0; sb < kSB; ++sb)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int s = 32 * sb + (i >> 2) * 16 + 4 * g4 + (i & 3);
-                outw[sb][i] = expf(gl * max(rows - s - e, 0));
-            }
+        for (int i = 0; i < 8; ++i) outw[i] = expf(gl * max(rows - ((i >> 2) * 16 + 4 * g4 + (i & 3)) - e, 0));
         grow = expm1f(gl * rows);
     };
-    weights(C);
+    weights(kLC);
 
     // ---- the entering state
     f32x4 st[kNT][JT], dst[kDg ? kNT : 1][kDg ? JT : 1];
@@ -342,45 +432,169 @@ __global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
             }
     }
 
-    const DRows<T, CHk> rowsk(r, g4);
-    const DCols<T, CHk> colsk(r, g4);
+    // ---- outputs: 4 neighbouring elements of a token a lane, in a buffer of 32 rows that goes along with the chunks
+    [[maybe_unused]] const int orow = H * p.Dv * (p.of32 ? 4 : S::kEs);
+    [[maybe_unused]] char* out = nullptr;
+    [[maybe_unused]] int to[2][JT];
+    if constexpr (kOut) {
+        out = static_cast<char*>(p.o) + (p.back ? it.start + it.len - kLC : it.start) * (int64_t)orow;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < JT; ++j) {
+                const int col = col0 + (wave * JT + j) * 16, row = 16 * t + r;
+                to[t][j] = col < p.Dv ? (p.back ? kLC - 1 - row : row) * orow + (h * p.Dv + col + 4 * g4) * (p.of32 ? 4 : S::kEs)
+                                      : kDropped;
+            }
+    }
+
+    LinearRows<T, CHk> rowsk(r, g4);
+    LinearCols<T, CHk> colsk(r, g4);
+    // this wavefront's columns of V (and X): down the rows, and quads along them
+    unsigned colv[JT];
+#pragma unroll
+    for (int j = 0; j < JT; ++j)
+        colv[j] = S::kAtV + DTile<CHv>::offset(4 * g4 + (r >> 2), 2 * (wave * JT + j) + ((r & 3) >> 1)) + (r & 1) * 8;
+    const unsigned scores = lds + kStages * S::kStage;
     [[maybe_unused]] float dg = 0.f;
 
-    for (int c = 0; c < nchunks; ++c) {
-        const unsigned stage = lds + (c & 1) * S::kStage;
-        wait_vmem();
-        __syncthreads();
-        if (c + 1 < nchunks) issue(c + 1, lds + ((c + 1) & 1) * S::kStage);
-        const int rows = min(C, it.len - c * C);
-        if (rows < C) weights(rows);
+    // Three wavefronts make the decayed scores of the chunk at `stage`, a 16 x 16 tile each (rows s, columns t), and leave
+    // them as operand quads.
+    auto x_quad = [&](unsigned stage, int row, int col, int rows) {
+        const int byte = col * S::kEs;
+        if constexpr (S::kHasX) {
+            return lds_quad(stage + S::kAtX + DTile<CHv>::offset(row, byte >> 4) + (byte & 15), T());
+        } else {
+            f32x4 v = {0.f, 0.f, 0.f, 0.f};
+            if (row < rows && col0 + col < p.Dv) v = *reinterpret_cast<const f32x4*>(xrows + row * p.x.row * S::kEs + byte);
+            return v;
+        }
+    };
+    auto make_scores = [&](unsigned stage, unsigned to_lds, int rows) {
+        if (wave >= 3) return;
+        f32x4 sc = {0.f, 0.f, 0.f, 0.f};
+        LinearRows<T, CHk> rq(r, g4), rk(r, g4);
+        rq.at(stage + tile_t * (16 * CHk * 16));
+        rk.at(stage + S::kAtK + tile_s * (16 * CHk * 16));
+        #pragma unroll
+        for (int kb = 0; kb < KB; ++kb) {
+            Vec8<T> qf, kf;
+            rq.load(qf, 0, 0, kb);
+            rk.load(kf, 0, 0, kb);
+            mma(sc, kf, qf);
+        }
+        if constexpr (kDg) {
+            // the pairs of tokens of this tile towards dg: X . V over this workgroup's columns, Q . K complete
+            f32x4 xv = {0.f, 0.f, 0.f, 0.f};
+            LinearRows<T, CHv> rx(r, g4), rv(r, g4);
+            rx.at(stage + S::kAtX + tile_t * (16 * CHv * 16));
+            rv.at(stage + S::kAtV + tile_s * (16 * CHv * 16));
+#pragma unroll
+            for (int kb = 0; kb < NW * JT / 2; ++kb) {
+                Vec8<T> xf, wf;
+                if constexpr (S::kHasX) {
+                    rx.load(xf, 0, 0, kb);
+                } else {
+                    const f32x4 x0 = x_quad(stage, 16 * tile_t + r, 32 * kb + 4 * g4, rows);
+                    const f32x4 x1 = x_quad(stage, 16 * tile_t + r, 32 * kb + 16 + 4 * g4, rows);
+#pragma unroll
+                    for (int m = 0; m < 4; ++m) { xf.set(m, x0[m]); xf.set(4 + m, x1[m]); }
+                }
+                rv.load(wf, 0, 0, kb);
+                mma(xv, wf, xf);
+            }
+#pragma unroll
+            for (int m = 0; m < 4; ++m) dg = fmaf(xv[m] * sc[m], tiled[m], dg);
+        }
+#pragma unroll
+        for (int m = 0; m < 4; ++m) sc[m] *= tilew[m];
+        // tile (0, 0) alone, then (1, 0) and (1, 1) side by side
+        lds_put(to_lds + (wave == 0 ? lane * 4 * S::kEs : (256 + lane * 8 + tile_s * 4) * S::kEs), sc, T());
+    };
 
-        Vec8<T> vf[kSB][JT];
+    wait_vmem();                                                  // the state's loads: not again in every chunk
+    if constexpr (S::kPipe) {
+        __syncthreads();
+        if (nchunks > 0) make_scores(lds, scores, kLC);
+    }
+    // the ring's offsets of this chunk and of the one whose copies start now
+    unsigned now = 0, next = (kStages - 1) * S::kStage, score = 0;
+    for (int c = 0; c < nchunks; ++c) {
+        // Memory operations complete in their order, so what was issued behind the copies that are needed may be outstanding:
+        // whole chunks' copies and, once as many have gone by, the stores of the chunks since.  Near the end, where
+        // copies are fewer, everything is waited for.
+        //   kPipe: chunk c + 1 (its scores are made now), issued kStages - 2 chunks ago; else chunk c, kStages - 1 ago
+        constexpr int kAgo = S::kPipe ? kStages - 2 : kStages - 1;
+        constexpr int kAhead = (kAgo - 1) * S::kCopies, kAll = kAhead + kAgo * S::kStores;
+        static_assert(kAll < 64, "vmcnt range");
+        if (c + kStages > nchunks) wait_vmem();
+        else if (c < kStages) wait_vmem_below<kAhead>();
+        else wait_vmem_below<kAll>();
+        __syncthreads();
+        const unsigned stage = lds + now;
+        now = now + S::kStage == kStages * S::kStage ? 0 : now + S::kStage;
+        if (c + kStages - 1 < nchunks) issue(lds + next);
+        next = stage - lds;
+        const int rows = min(kLC, it.len - c * kLC);
+        if (rows < kLC) weights(rows);
+        unsigned made = scores;
+        if constexpr (S::kPipe) {
+            made += score;
+            score = S::kScores - score;
+            if (c + 1 < nchunks) make_scores(lds + now, scores + score, kLC);
+        } else if constexpr (kOut) {
+            make_scores(stage, scores, rows);
+            __syncthreads();
+        }
+        rowsk.at(stage);
+        colsk.at(stage);
+
+        Vec8<T> vf[JT];
 #pragma unroll
-        for (int sb = 0; sb < kSB; ++sb)
+        for (int j = 0; j < JT; ++j) {
+            if constexpr (sizeof(T) == 2) {
+                typedef short v4i16 __attribute__((ext_vector_type(4)));
+                typedef __attribute__((address_space(3))) v4i16* P;
+                const unsigned o = colv[j] + stage;
+                const v4i16 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(uintptr_t)o);
+                const v4i16 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((P)(uintptr_t)(o + 16 * CHv * 16));
+                vf[j].v = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+            } else {
+                DCols<T, CHv>::load_any(vf[j], stage + S::kAtV, wave * JT + j, r, g4);
+            }
+        }
+
+        // operands of the state's products, kAheadK at a time before they are needed
+        constexpr int kAheadK = sizeof(T) == 2 ? (kNT < 4 ? kNT : 4) : 1;
+        Vec8<T> kt[kAheadK];
+        auto load_first = [&]() {
 #pragma unroll
-            for (int j = 0; j < JT; ++j)
-                DCols<T, CHv>::load_any(vf[sb][j], stage + S::kAtV + sb * S::kV, wave * JT + j, r, g4);
+            for (int i = 0; i < kAheadK; ++i) colsk.load(kt[i], S::kAtK, i);
+        };
 
         if constexpr (kOut) {
-            f32x4 acc[kTT][JT], sc[kTT * (kTT + 1) / 2], dacc[kDg ? kTT : 1][kDg ? JT : 1];
+            f32x4 acc[2][JT], dacc[kDg ? 2 : 1][kDg ? JT : 1];
 #pragma unroll
-            for (int t = 0; t < kTT; ++t)
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < JT; ++j) {
                     acc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
                     if constexpr (kDg) dacc[t][j] = f32x4{0.f, 0.f, 0.f, 0.f};
                 }
-#pragma unroll
-            for (int i = 0; i < kTT * (kTT + 1) / 2; ++i) sc[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-            // against the entering state, and the scores (rows s, columns t)
+            // against the entering state
+            Vec8<T> qf[2][2], sf[2];
+            rowsk.load(qf[0][0], 0, 0, 0);
+            rowsk.load(qf[0][1], 0, 1, 0);
 #pragma unroll
             for (int kb = 0; kb < KB; ++kb) {
-                Vec8<T> qf[kTT], kf[kTT];
-#pragma unroll
-                for (int t = 0; t < kTT; ++t) {
-                    rowsk.load(qf[t], stage + (t >> 1) * S::kQK, t & 1, kb);
-                    rowsk.load(kf[t], stage + S::kAtK + (t >> 1) * S::kQK, t & 1, kb);
+                if (kb + 1 < KB) {
+                    rowsk.load(qf[(kb + 1) & 1][0], 0, 0, kb + 1);
+                    rowsk.load(qf[(kb + 1) & 1][1], 0, 1, kb + 1);
+                } else {
+                    lds_half(sf[0], made + lane * 4 * S::kEs);
+                    lds_frag(sf[1], made + (256 + lane * 8) * S::kEs);
                 }
+                __builtin_amdgcn_sched_barrier(0);                // the next operands are on the way
 #pragma unroll
                 for (int j = 0; j < JT; ++j) {
                     float s8[8];
@@ -394,130 +608,68 @@ __global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
                         for (int m = 0; m < 4; ++m) { s8[m] = dst[2 * kb][j][m]; s8[4 + m] = dst[2 * kb + 1][j][m]; }
                         df.set(s8);
 #pragma unroll
-                        for (int t = 0; t < kTT; ++t) {
-                            mma_px(acc[t][j], f, qf[t]);
-                            mma_px(dacc[t][j], df, qf[t]);
+                        for (int t = 0; t < 2; ++t) {
+                            mma_px(acc[t][j], f, qf[kb & 1][t]);
+                            mma_px(dacc[t][j], df, qf[kb & 1][t]);
                         }
                     } else {
                         Vec8<T> f;
                         pack8(f, s8);
 #pragma unroll
-                        for (int t = 0; t < kTT; ++t) mma(acc[t][j], f, qf[t]);
+                        for (int t = 0; t < 2; ++t) mma(acc[t][j], f, qf[kb & 1][t]);
                     }
                 }
-#pragma unroll
-                for (int t = 0; t < kTT; ++t)
-#pragma unroll
-                    for (int s = 0; s <= t; ++s) mma(sc[t * (t + 1) / 2 + s], kf[s], qf[t]);
             }
-            float at = into;                                      // a^(t + e), 16 tokens on with every tile
+            load_first();
+            __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-            for (int t = 0; t < kTT; ++t) {
-                if constexpr (kDg) {
+            for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int j = 0; j < JT; ++j) {
-                        const int tile = wave * JT + j;
-                        const f32x4 x = lds_quad(stage + S::kAtX + (t >> 1) * S::kV +
-                                                     DTile<CHv>::offset((t & 1) * 16 + r, (tile * 16 + 4 * g4) * S::kEs / 16) +
-                                                     ((tile * 16 + 4 * g4) * S::kEs & 15), T());
+                for (int j = 0; j < JT; ++j) {
+                    if constexpr (kDg) {
+                        const f32x4 x = x_quad(stage, 16 * t + r, (wave * JT + j) * 16 + 4 * g4, rows);
                         float sum = 0.f;
 #pragma unroll
                         for (int m = 0; m < 4; ++m)
                             sum = fmaf(x[m], fmaf((float)(16 * t + r + 1), acc[t][j][m], dacc[t][j][m]), sum);
-                        dg = fmaf(at, sum, dg);
+                        dg = fmaf(t ? into1 : into0, sum, dg);
                     }
+                    acc[t][j] *= t ? into1 : into0;
+                    mma(acc[t][j], vf[j], sf[t]);                  // the chunk's own scores
                 }
+            {
+                const __amdgpu_buffer_rsrc_t buf = __builtin_amdgcn_make_buffer_rsrc(out, 0, kLC * orow, kBufferDword3);
+                auto store = [&](auto type) {
 #pragma unroll
-                for (int j = 0; j < JT; ++j) acc[t][j] *= at;
-                at *= a16;
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int j = 0; j < JT; ++j)           // (rows behind the walk's end are dropped: always as many stores)
+                            buffer_store4(buf, 16 * t + r < rows ? to[t][j] : kDropped, 0, acc[t][j], type);
+                };
+                if (p.of32) store(0.f);
+                else store(T());
+                out += p.back ? -(int64_t)kLC * orow : (int64_t)kLC * orow;
             }
-            if constexpr (kDg) {
-                // the chunk's own pairs: X . V over this wavefront's 32 columns, Q . K complete
-                static_assert(JT == 2, "a wavefront's columns are one contraction block");
-                Vec8<T> xf[kTT], wf[kTT];
-#pragma unroll
-                for (int t = 0; t < kTT; ++t) {
-                    linear_rows_any<T, CHv>(xf[t], stage + S::kAtX + (t >> 1) * S::kV, t & 1, wave, r, g4);
-                    linear_rows_any<T, CHv>(wf[t], stage + S::kAtV + (t >> 1) * S::kV, t & 1, wave, r, g4);
-                }
-#pragma unroll
-                for (int t = 0; t < kTT; ++t) {
-                    float far = 1.f;
-#pragma unroll
-                    for (int s = t; s >= 0; --s) {
-                        f32x4 xv = {0.f, 0.f, 0.f, 0.f};
-                        mma(xv, wf[s], xf[t]);
-                        const f32x4 qk = sc[t * (t + 1) / 2 + s];
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const int gap = 16 * (t - s) + r - 4 * g4 - m;
-                            const float w = s == t ? diag[m] : off[m] * far;
-                            const float term = xv[m] * qk[m] * (w * gap);
-                            dg += s == t ? select(gap > 0, term, 0.f) : term;
-                        }
-                        if (s < t) far *= a16;
-                    }
-                }
-            }
-            // the chunk's own scores, decayed
-#pragma unroll
-            for (int t = 0; t < kTT; ++t) {
-#pragma unroll
-                for (int sb = 0; sb <= t / 2; ++sb) {
-                    float w8[8];
-#pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        const int s = 2 * sb + x;
-                        float far = 1.f;
-#pragma unroll
-                        for (int i = s + 1; i < t; ++i) far *= a16;
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            if (s > t) w8[4 * x + m] = 0.f;
-                            else if (s == t) w8[4 * x + m] = select(r >= 4 * g4 + m, sc[t * (t + 1) / 2 + min(s, t)][m] * diag[m], 0.f);
-                            else w8[4 * x + m] = sc[t * (t + 1) / 2 + min(s, t)][m] * (off[m] * far);
-                        }
-                    }
-                    Vec8<T> f;
-                    pack8(f, w8);
-#pragma unroll
-                    for (int j = 0; j < JT; ++j) mma(acc[t][j], vf[sb][j], f);
-                }
-            }
-            // rows Dv, columns t: 4 neighbouring elements of a token a lane
-#pragma unroll
-            for (int t = 0; t < kTT; ++t) {
-                const int row = 16 * t + r;
-                const int64_t tok = p.back ? it.start + it.len - 1 - (c * C + row) : it.start + c * C + row;
-#pragma unroll
-                for (int j = 0; j < JT; ++j) {
-                    const int col = col0 + (wave * JT + j) * 16 + 4 * g4;
-                    if (row < rows && col < p.Dv) {
-                        const int64_t to = (tok * H + h) * p.Dv + col;
-                        if (p.of32) store4((float*)p.o + to, acc[t][j][0], acc[t][j][1], acc[t][j][2], acc[t][j][3]);
-                        else store4((T*)p.o + to, acc[t][j][0], acc[t][j][1], acc[t][j][2], acc[t][j][3]);
-                    }
-                }
-            }
+            if constexpr (kDg && !S::kHasX) xrows += step[3];
+        } else {
+            load_first();
         }
 
         // the state behind the chunk: fp32 results, so the weighted values are pairs
-        Pair<T> vw[kSB][JT], dvw[kDg ? kSB : 1][kDg ? JT : 1];
+        Pair<T> vw[JT], dvw[kDg ? JT : 1];
 #pragma unroll
-        for (int sb = 0; sb < kSB; ++sb)
+        for (int j = 0; j < JT; ++j) {
+            float w8[8];
 #pragma unroll
-            for (int j = 0; j < JT; ++j) {
-                float w8[8];
+            for (int i = 0; i < 8; ++i) w8[i] = vf[j].get(i) * outw[i];
+            vw[j].set(w8);
+            if constexpr (kDg) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i) w8[i] = vf[sb][j].get(i) * outw[sb][i];
-                vw[sb][j].set(w8);
-                if constexpr (kDg) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        w8[i] = vf[sb][j].get(i) * (outw[sb][i] * (float)(rows - 1 - (32 * sb + (i >> 2) * 16 + 4 * g4 + (i & 3))));
-                    dvw[sb][j].set(w8);
-                }
+                for (int i = 0; i < 8; ++i)
+                    w8[i] = vf[j].get(i) * (outw[i] * (float)(rows - 1 - ((i >> 2) * 16 + 4 * g4 + (i & 3))));
+                dvw[j].set(w8);
             }
+        }
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
@@ -529,30 +681,23 @@ __global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
                 }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) st[nt][j][m] = fmaf(st[nt][j][m], grow, st[nt][j][m]);
+                mma_xp(st[nt][j], kt[nt % kAheadK], vw[j]);
+                if constexpr (kDg) mma_xp(dst[nt][j], kt[nt % kAheadK], dvw[j]);
             }
-#pragma unroll
-            for (int sb = 0; sb < kSB; ++sb) {
-                Vec8<T> kf;
-                colsk.load(kf, stage + S::kAtK + sb * S::kQK, nt);
-#pragma unroll
-                for (int j = 0; j < JT; ++j) {
-                    mma_xp(st[nt][j], kf, vw[sb][j]);
-                    if constexpr (kDg) mma_xp(dst[nt][j], kf, dvw[sb][j]);
-                }
-            }
+            if (nt + kAheadK < kNT) colsk.load(kt[nt % kAheadK], S::kAtK, nt + kAheadK);
         }
-        settle();
     }
+    settle();
 
     // ---- the state at the end
     if constexpr (kOut) {
         if (ends) {
             if (p.fin) {
-                float* to = p.fin + (it.row * H + h) * PN;
+                float* at = p.fin + (it.row * H + h) * PN;
 #pragma unroll
                 for (int nt = 0; nt < kNT; ++nt)
 #pragma unroll
-                    for (int j = 0; j < JT; ++j) store_state(to, st[nt][j], nt, j);
+                    for (int j = 0; j < JT; ++j) store_state(at, st[nt][j], nt, j);
             }
             if constexpr (kDg) {
                 const float* last = p.dlast ? p.dlast + (it.row * H + h) * PN : nullptr;
@@ -584,22 +729,22 @@ __global__ __launch_bounds__(NW * 64) void linear_walk_kernel(LinearWalk<T> p)
 
 // ---- launches -------------------------------------------------------------------------------------------
 
-template <typename T, int KB, int NW, int JT, int C, bool kOut, bool kDg>
+template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
 hipError_t launch_walk(const LinearWalk<T>& p, hipStream_t stream)
 {
-    using S = LinearShape<T, KB, NW, JT, C, kOut, kDg>;
-    static_assert(2 * S::kStage <= 160 * 1024, "two stages of LDS");
+    using S = LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>;
+    static_assert(S::kLds <= 160 * 1024, "the ring fits LDS");
     const int64_t slices = (p.Dv + NW * JT * 16 - 1) / (NW * JT * 16);
     const int64_t blocks = linear_items(p.d, p.seg) * p.d.nheads * slices;
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL((linear_walk_kernel<T, KB, NW, JT, C, kOut, kDg>), dim3((unsigned)blocks), dim3(NW * 64),
-                       2 * S::kStage, stream, p);
+    hipLaunchKernelGGL((linear_walk_kernel<T, KB, NW, JT, kBudget, kOut, kDg>), dim3((unsigned)blocks), dim3(NW * 64),
+                       S::kLds, stream, p);
     return hipGetLastError();
 }
 
 // Columns of the state that a workgroup of a walk holds (kDg: of a walk towards dg), and wavefronts it has.
 constexpr int linear_columns(int elem_bytes, bool dg, int Dv) { return elem_bytes == 2 && Dv > 64 ? 128 : 64; }
-constexpr int linear_waves(int elem_bytes, bool dg, int Dv) { return dg ? linear_columns(elem_bytes, dg, Dv) / 32 : 4; }
+constexpr int linear_waves(int elem_bytes, bool dg, int Dv) { return dg ? linear_columns(elem_bytes, dg, Dv) / 16 : 4; }
 
 template <typename T, bool kOut, bool kDg>
 hipError_t launch_linear_walk(const LinearWalk<T>& p, hipStream_t stream);
