@@ -4,7 +4,7 @@
 // The forward is one walk.  The backward is three: dq forwards, with the sums of dg; dk and dv backwards.  Where there are
 // fewer walks than the GPU holds, rows are cut into segments: a first pass leaves what every segment but the last adds to
 // the state, linear_join_kernel turns that into the states that enter them, and the walk runs over all segments
-// at once.
+// at once.  Where there are a few too many, segments follow each other in a chain (see linear_cut).
 #include <algorithm>
 
 #include "linear_walk.hpp"
@@ -96,41 +96,48 @@ unsigned blocks_of(int64_t threads) { return (unsigned)((threads + 255) / 256); 
 
 size_t bytes_up(int64_t floats) { return ((size_t)floats * 4 + 255) / 256 * 256; }
 
-// Tokens of a segment.  A walk takes one workgroup; two fit a CU.
-int64_t linear_segment(const DeltaDims& d, int64_t slices)
-{
-    constexpr int64_t kCUs = 256, kLeast = 256;
-    const int64_t walks = d.seqs * d.nheads * slices;
-    int64_t seg;
-    if (d.cu) {
-        seg = std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
-    } else {
-        if (walks == 0 || walks >= kCUs) return kWholeRows;
-        const int64_t n = std::min<int64_t>(2 * kCUs / walks, d.seqlen / kLeast);
-        if (n <= 1) return kWholeRows;
-        seg = (d.seqlen + n - 1) / n;
-    }
-    seg = (seg + 63) / 64 * 64;
-    return (d.cu ? d.tokens : d.seqlen) <= seg ? kWholeRows : seg;
-}
-
-int64_t forward_segment(const DeltaDims& d, int elem_bytes)
-{
-    const int columns = linear_columns(elem_bytes, false, (int)d.headdim);
-    return linear_segment(d, (d.headdim + columns - 1) / columns);
-}
-
 int64_t state_floats(const DeltaDims& d, int64_t items) { return items * d.nheads * d.headdim * d.dstate; }
 
-// The walk, or where rows are cut its three steps; states: room for the items' states (kDg: twice that).
-template <typename T, bool kDg>
-hipError_t walk(LinearWalk<T> p, const float* enter, float* states, hipStream_t stream)
+// How the rows of a walk are run: whole, cut into segments that walk at once (with a pass before), or in a chain.
+struct Cut {
+    int64_t seg;
+    bool chain;
+};
+
+__global__ __launch_bounds__(256) void linear_zero_kernel(unsigned* p, int64_t n)
 {
-    const bool cut = p.seg != kWholeRows;
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) p[i] = 0;
+}
+
+// Bytes of workspace for one walk: the items' states (dg: twice that), or a chain's counters and states.
+size_t walk_bytes(const DeltaDims& d, const Cut& c, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
+{
+    if (c.seg == kWholeRows) return 0;
+    const int64_t columns = linear_columns(elem_bytes, dg, (int)Dv), walks = d.seqs * d.nheads * ((Dv + columns - 1) / columns);
+    if (c.chain) return bytes_up(walks + 1) + bytes_up(d.seqs * d.nheads * linear_handed(elem_bytes, dg, Dk, Dv));
+    return (dg ? 2 : 1) * bytes_up(state_floats(d, linear_items(d, c.seg)));
+}
+
+// The walk, or where rows are cut its steps.
+template <typename T, bool kDg>
+hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states, hipStream_t stream)
+{
+    p.seg = c.seg;
     p.enter = enter;
     p.denter = nullptr;
     p.by_item = false;
-    if (cut) {
+    p.ticket = nullptr;
+    if (c.seg != kWholeRows && c.chain) {
+        const int64_t columns = linear_columns(sizeof(T), kDg, p.Dv);
+        const int64_t words = p.d.seqs * p.d.nheads * ((p.Dv + columns - 1) / columns) + 1;
+        p.ticket = reinterpret_cast<unsigned*>(states);
+        p.done = p.ticket + 1;
+        p.handed = states + bytes_up(words) / 4;
+        hipLaunchKernelGGL(linear_zero_kernel, dim3(blocks_of(words)), dim3(256), 0, stream, p.ticket, words);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    } else if (c.seg != kWholeRows) {
         const int64_t PN = p.d.headdim * p.d.dstate;
         LinearWalk<T> first = p;
         first.fin = states;
@@ -147,24 +154,68 @@ hipError_t walk(LinearWalk<T> p, const float* enter, float* states, hipStream_t 
     return launch_linear_walk<T, true, kDg>(p, stream);
 }
 
+// A workgroup walks one slice of a row and head.  Measured with heads of 64 x 128 over 4096 tokens in bf16, where one row
+// alone takes a CU 175 us, two on one 332:
+//  - fewer walks than CUs: rows are cut into segments that walk at once, for a pass over K and V more (128 walks: 117 us,
+//    whole 139).
+//  - some more than CUs: a few CUs would have one more than the others from the first token to the last. In a chain
+//    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
+//    525, 558; backward of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
+//    the starts are worth.
+//  - rows of different lengths: the same, in pieces of 1024 tokens (7 of 64 to 4096 tokens, 80 heads: 230 us, cut at
+//    once 346; 37 of up to 150, 16 heads of 128 x 128, 40 and 61). With few walks one long row would walk alone (256
+//    walks of up to 16384 tokens: 503 against 454), with many all CUs are busy in any case (2048 walks: 141, whole 128).
+Cut linear_cut(const DeltaDims& d, int64_t slices)
+{
+    constexpr int64_t kCUs = 256, kLeast = 256;
+    const int64_t walks = d.seqs * d.nheads * slices, over = walks % (2 * kCUs);
+    Cut c{kWholeRows, false};
+    if (d.cu) {
+        if (walks >= 4 * kCUs) return c;
+        c.chain = walks >= 3 * kCUs / 2 && d.seqs <= kChainRows;
+        c.seg = c.chain ? 1024 : std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
+    } else if (walks < kCUs) {
+        const int64_t n = walks > 0 ? std::min<int64_t>(2 * kCUs / walks, d.seqlen / kLeast) : 1;
+        if (n <= 1) return c;
+        c.seg = (d.seqlen + n - 1) / n;
+    } else if (walks > kCUs && walks < 4 * kCUs && over > 0 && over <= 3 * kCUs / 2 && d.seqlen >= 8 * kLeast) {
+        const int64_t n = walks < 11 * kCUs / 8 ? 3 : 2;
+        c.seg = (d.seqlen + n - 1) / n;
+        c.chain = true;
+    } else {
+        return c;
+    }
+    c.seg = (c.seg + 63) / 64 * 64;
+    if ((d.cu ? d.tokens : d.seqlen) <= c.seg) return Cut{kWholeRows, false};
+    return c;
+}
+
+Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dv)
+{
+    const int columns = linear_columns(elem_bytes, dg, (int)Dv);
+    return linear_cut(d, (Dv + columns - 1) / columns);
+}
+
 struct GradLayout {
-    int64_t seg, items;
+    Cut cq, ck, cv;
+    int64_t items;           // of the walk for dq
     int parts;
-    size_t states, dpart, dk, dv, total;
+    size_t dpart, dk, dv, total;
 };
 
 GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
 {
     GradLayout l;
-    // the same segments for all three walks, by the one with the fewest workgroups
-    const int64_t most = std::max<int64_t>(linear_columns(elem_bytes, false, (int)d.headdim),
-                                           linear_columns(elem_bytes, true, (int)d.dstate));
-    l.seg = linear_segment(d, std::max<int64_t>(1, std::min(d.headdim, d.dstate) / most));
-    l.items = linear_items(d, l.seg);
+    l.cq = walk_cut(d, elem_bytes, true, d.dstate);
+    l.ck = walk_cut(d, elem_bytes, false, d.dstate);
+    l.cv = walk_cut(d, elem_bytes, false, d.headdim);
+    l.items = linear_items(d, l.cq.seg);
     const int columns = linear_columns(elem_bytes, true, (int)d.dstate);
     l.parts = (int)((d.dstate + columns - 1) / columns) * linear_waves(elem_bytes, true, (int)d.dstate);
-    l.states = 0;
-    l.dpart = l.states + (l.seg == kWholeRows ? 0 : 2 * bytes_up(state_floats(d, l.items)));
+    // (the walks run one after another: one room for their states)
+    l.dpart = std::max({walk_bytes(d, l.cq, elem_bytes, true, d.headdim, d.dstate),
+                        walk_bytes(d, l.ck, elem_bytes, false, d.headdim, d.dstate),
+                        walk_bytes(d, l.cv, elem_bytes, false, d.dstate, d.headdim)});
     l.dk = l.dpart + bytes_up(l.items * d.nheads * l.parts);
     const bool shared = d.nheads != d.ngroups;
     l.dv = l.dk + (shared ? bytes_up(d.tokens * d.nheads * d.dstate) : 0);
@@ -176,16 +227,21 @@ GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
 
 size_t linear_forward_workspace(const DeltaDims& d, int elem_bytes)
 {
-    const int64_t seg = forward_segment(d, elem_bytes);
-    return 256 + (seg == kWholeRows ? 0 : bytes_up(state_floats(d, linear_items(d, seg))));
+    return 256 + walk_bytes(d, walk_cut(d, elem_bytes, false, d.headdim), elem_bytes, false, d.dstate, d.headdim);
 }
 
 size_t linear_backward_workspace(const DeltaDims& d, int elem_bytes) { return grad_layout(d, elem_bytes).total; }
 
 int64_t linear_blocks(const DeltaDims& d, int elem_bytes)
 {
-    const int64_t seg = std::min(forward_segment(d, elem_bytes), grad_layout(d, elem_bytes).seg);
-    return linear_items(d, seg) * d.nheads * ((std::max(d.headdim, d.dstate) + 63) / 64);
+    int64_t most = 0;
+    for (const bool dg : {false, true})
+        for (const int64_t Dv : {d.headdim, d.dstate}) {
+            const int columns = linear_columns(elem_bytes, dg, (int)Dv);
+            most = std::max(most, linear_items(d, walk_cut(d, elem_bytes, dg, Dv).seg) * d.nheads * ((Dv + columns - 1) / columns) *
+                                      (linear_waves(elem_bytes, dg, (int)Dv) > 4 ? 2 : 1));
+        }
+    return most;
 }
 
 template <typename T>
@@ -205,8 +261,7 @@ hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T
     p.Dk = (int)d.dstate;
     p.Dv = (int)d.headdim;
     p.d = d;
-    p.seg = forward_segment(d, sizeof(T));
-    return walk<T, false>(p, init, static_cast<float*>(workspace), stream);
+    return walk<T, false>(p, walk_cut(d, sizeof(T), false, d.headdim), init, static_cast<float*>(workspace), stream);
 }
 
 template <typename T>
@@ -216,7 +271,7 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
 {
     const GradLayout l = grad_layout(d, sizeof(T));
     char* ws = static_cast<char*>(workspace);
-    float* states = reinterpret_cast<float*>(ws + l.states);
+    float* states = reinterpret_cast<float*>(ws);
     float* dpart = reinterpret_cast<float*>(ws + l.dpart);
     const int share = (int)(d.nheads / d.ngroups);
     const bool shared = share > 1;
@@ -225,7 +280,6 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     LinearWalk<T> p{};
     p.g = g;
     p.d = d;
-    p.seg = l.seg;
     // dq: the rows of the walk's state are the state's rows, its columns the columns
     p.q = od;
     p.k = ov;
@@ -238,7 +292,7 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     p.Dv = (int)d.dstate;
     p.dlast = dfinal;
     p.dpart = dpart;
-    hipError_t e = walk<T, true>(p, init, states, stream);
+    hipError_t e = walk<T, true>(p, l.cq, init, states, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(linear_dg_kernel, dim3((unsigned)d.nheads), dim3(256), 0, stream, dpart, dg, l.items, d.nheads,
                        l.parts);
@@ -253,7 +307,7 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     p.back = true;
     p.of32 = shared;
     p.o = shared ? static_cast<void*>(ws + l.dk) : dk;
-    if ((e = walk<T, false>(p, dfinal, states, stream)) != hipSuccess) return e;
+    if ((e = walk<T, false>(p, l.ck, dfinal, states, stream)) != hipSuccess) return e;
     // dv, and the gradient of the state before the first token
     p.q = ok;
     p.k = oq;
@@ -264,7 +318,7 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     p.Dk = (int)d.dstate;
     p.Dv = (int)d.headdim;
     p.fin = dinit;
-    if ((e = walk<T, false>(p, dfinal, states, stream)) != hipSuccess) return e;
+    if ((e = walk<T, false>(p, l.cv, dfinal, states, stream)) != hipSuccess) return e;
     if (shared && d.tokens > 0) {
         const int64_t rows = d.tokens * d.ngroups;
         hipLaunchKernelGGL((linear_group_kernel<T>), dim3(blocks_of(rows * d.dstate / 4)), dim3(256), 0, stream,

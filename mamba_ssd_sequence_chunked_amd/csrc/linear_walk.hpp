@@ -29,8 +29,11 @@
 // chunk, and the registers do not hold what is read ahead.
 //
 // A row may be cut into segments that walk at the same time: a first pass of the same kernel (states only) leaves
-// what each adds to the state, linear_join carries the states over, and the walk starts each segment from its own.
+// what each adds to the state, linear_join carries the states over, and the walk starts each segment from its own.  Or
+// into a chain: one launch in which a segment takes over the state when the one before it is done.
 #pragma once
+
+#include <algorithm>
 
 #include "delta_tiles.hpp"
 
@@ -60,6 +63,11 @@ template <typename T> struct LinearWalk {
     bool back;               // from the last token to the first
     DeltaDims d;
     int64_t seg;             // tokens of a segment (a multiple of 64)
+    // Segments one after another (chained): a ticket counter and a count of each walk's segments that are done, all zero, and
+    // room for each walk's state as fragments.  Null: all segments at once.
+    unsigned* ticket;
+    unsigned* done;
+    float* handed;
 };
 
 // ---- rows and segments ----------------------------------------------------------------------------------
@@ -119,6 +127,46 @@ __device__ __forceinline__ bool linear_item(const DeltaDims& d, int64_t seg, int
     it.first = i == 0;
     it.last = (i + 1) * seg >= n;
     return true;
+}
+
+// A chain's task j in the order first segments of all rows, second segments, ...: its row and which segment of that it is.
+// At most kChainRows rows of different lengths, four to a lane; false where there is no such task.
+constexpr int kChainRows = 256;
+__device__ __forceinline__ bool linear_task(const DeltaDims& d, int64_t seg, int j, LinearItem& it, unsigned& turn)
+{
+    int len[kChainRows / 64];
+#pragma unroll
+    for (int k = 0; k < kChainRows / 64; ++k) {
+        const int64_t s = 64 * k + lane_id();
+        len[k] = -1;
+        if (s < d.seqs) {
+            const int64_t begin = linear_offset(d, s);
+            len[k] = (int)(max(linear_offset(d, s + 1), begin) - begin);
+        }
+    }
+    // (a row without tokens has one segment, without tokens)
+    for (int64_t from = 0;; from += seg) {
+        int any = 0;
+#pragma unroll
+        for (int k = 0; k < kChainRows / 64; ++k) {
+            const uint64_t has = __ballot(from == 0 ? len[k] >= 0 : len[k] > from);
+            const int count = __popcll(has);
+            if (j < count) {
+                const uint64_t mine = __ballot((has >> lane_id() & 1) && __popcll(has & ((uint64_t(1) << lane_id()) - 1)) == j);
+                it.row = 64 * k + __builtin_ctzll(mine);
+                const int64_t begin = linear_offset(d, it.row), n = max(linear_offset(d, it.row + 1), begin) - begin;
+                turn = (unsigned)(from / seg);
+                it.start = begin + from;
+                it.len = (int)min(n - from, seg);
+                it.first = from == 0;
+                it.last = from + seg >= n;
+                return true;
+            }
+            j -= count;
+            any += count;
+        }
+        if (any == 0) return false;
+    }
 }
 
 // ---- copies ---------------------------------------------------------------------------------------------
@@ -188,7 +236,7 @@ template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg> 
     // three 16 x 16 tiles of decayed scores as operand quads
     static constexpr int kScores = kOut ? 3 * 64 * 4 * kEs : 0;
     static constexpr int kFit = (kBudget - 2 * kScores) / kStage;
-    static constexpr int kStages = kFit < 2 ? 2 : kFit > 4 ? 4 : kFit;
+    static constexpr int kStages = kFit < 2 ? 2 : kFit > 3 ? 3 : kFit;
     static constexpr bool kPipe = kOut && kStages > 2;                // a chunk's scores are made while the one before is read
     static constexpr int kLds = kStages * kStage + (kPipe ? 2 : 1) * kScores;
     // what every wavefront issues at least: copies for a chunk, stores of a chunk's outputs
@@ -314,13 +362,42 @@ void linear_walk_kernel(LinearWalk<T> p)
     const int r = lane & 15, g4 = lane >> 4;
 
     const int slices = (p.Dv + NW * JT * 16 - 1) / (NW * JT * 16);
-    int64_t n = xcd_logical_block(blockIdx.x, gridDim.x);
-    const int slice = (int)(n % slices);
-    n /= slices;
-    const int H = (int)p.d.nheads, h = (int)(n % H);
-    const int64_t item = n / H;
+    const int H = (int)p.d.nheads;
+    const bool chained = kOut && p.ticket;
     LinearItem it;
-    if (!linear_item(p.d, p.seg, item, it)) return;
+    int at;
+    unsigned walk = 0, turn = 0;                                  // a segment's place in its chain
+    if (chained) {
+        // Workgroups take the segments in the order in which they start: all rows' first ones, all second ones and so on.  The
+        // one that a segment waits for was taken before, so its workgroup runs: no wait is for one that has not started.
+        if (threadIdx.x == 0) *(__attribute__((address_space(3))) unsigned*)(uintptr_t)lds = atomicAdd(p.ticket, 1u);
+        __syncthreads();
+        const unsigned mine = __builtin_amdgcn_readfirstlane(lds_at<unsigned>(lds));
+        __syncthreads();
+        const unsigned of_row = H * slices;
+        if (p.d.cu) {
+            const unsigned j = __builtin_amdgcn_readfirstlane(mine / of_row);
+            if (!linear_task(p.d, p.seg, (int)j, it, turn)) return;
+            turn = __builtin_amdgcn_readfirstlane(turn);
+            it.row = __builtin_amdgcn_readfirstlane((int)it.row);
+            it.start = __builtin_amdgcn_readfirstlane((int)it.start);
+            it.len = __builtin_amdgcn_readfirstlane(it.len);
+            walk = (unsigned)it.row * of_row + xcd_logical_block((int)(mine - j * of_row), (int)of_row);
+            at = walk;
+        } else {
+            const unsigned walks = (unsigned)p.d.seqs * of_row;
+            turn = __builtin_amdgcn_readfirstlane(mine / walks);
+            walk = __builtin_amdgcn_readfirstlane(xcd_logical_block((int)(mine - turn * walks), (int)walks));
+            const unsigned per = __builtin_amdgcn_readfirstlane(gridDim.x / walks), row = walk / of_row;
+            at = (row * per + (p.back ? per - 1 - turn : turn)) * of_row + (walk - row * of_row);
+        }
+    } else {
+        at = xcd_logical_block(blockIdx.x, gridDim.x);
+    }
+    at = __builtin_amdgcn_readfirstlane(at);                      // (fewer than 2^24 workgroups)
+    const int slice = at % slices, h = at / slices % H;
+    const int64_t item = at / slices / H;
+    if (!(chained && p.d.cu) && !linear_item(p.d, p.seg, item, it)) return;
     const bool ends = p.back ? it.first : it.last;                // no segment of the row walks on from this one
     if (!kOut && ends) return;
 
@@ -420,7 +497,40 @@ void linear_walk_kernel(LinearWalk<T> p)
             }
         }
     };
-    {
+    // the state between two segments of a chain, as fragments, written and read past the caches of one XCD
+    constexpr int kFrag = NW * 64 * 4;
+    float* const handed = p.handed + (int64_t)walk * ((kDg ? 2 : 1) * kNT * JT * kFrag) + threadIdx.x * 4;
+    auto take = [&](int i) {
+        f32x4 v;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint64_t w = __hip_atomic_load(reinterpret_cast<const uint64_t*>(handed + (int64_t)i * kFrag) + x, __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT);
+            v[2 * x] = __uint_as_float((unsigned)w);
+            v[2 * x + 1] = __uint_as_float((unsigned)(w >> 32));
+        }
+        return v;
+    };
+    auto hand = [&](int i, const f32x4& v) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+            __hip_atomic_store(reinterpret_cast<uint64_t*>(handed + (int64_t)i * kFrag) + x,
+                               (uint64_t)__float_as_uint(v[2 * x + 1]) << 32 | __float_as_uint(v[2 * x]), __ATOMIC_RELAXED,
+                               __HIP_MEMORY_SCOPE_AGENT);
+    };
+    if (chained && turn > 0) {
+        if (threadIdx.x == 0)
+            while (__hip_atomic_load(p.done + walk, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < turn)
+                __builtin_amdgcn_s_sleep(8);
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+            for (int j = 0; j < JT; ++j) {
+                st[nt][j] = take(nt * JT + j);
+                if constexpr (kDg) dst[nt][j] = take((kNT + nt) * JT + j);
+            }
+    } else {
         const float* in = kOut && p.enter ? p.enter + ((p.by_item ? item : it.row) * H + h) * PN : nullptr;
         const float* din = kOut && kDg && p.denter ? p.denter + (item * H + h) * PN : nullptr;
 #pragma unroll
@@ -691,6 +801,19 @@ void linear_walk_kernel(LinearWalk<T> p)
 
     // ---- the state at the end
     if constexpr (kOut) {
+        if (chained && !ends) {
+#pragma unroll
+            for (int nt = 0; nt < kNT; ++nt)
+#pragma unroll
+                for (int j = 0; j < JT; ++j) {
+                    hand(nt * JT + j, st[nt][j]);
+                    if constexpr (kDg) hand((kNT + nt) * JT + j, dst[nt][j]);
+                }
+            wait_vmem();                                          // every wavefront's part has arrived
+            __syncthreads();
+            if (threadIdx.x == 0)
+                __hip_atomic_store(p.done + walk, turn + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        }
         if (ends) {
             if (p.fin) {
                 float* at = p.fin + (it.row * H + h) * PN;
@@ -738,13 +861,21 @@ hipError_t launch_walk(const LinearWalk<T>& p, hipStream_t stream)
     const int64_t blocks = linear_items(p.d, p.seg) * p.d.nheads * slices;
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((linear_walk_kernel<T, KB, NW, JT, kBudget, kOut, kDg>), dim3((unsigned)blocks), dim3(NW * 64),
-                       S::kLds, stream, p);
+                       // (a chain's segments one to a CU: one that waits takes no other's turn)
+                       p.ticket ? std::max(S::kLds, 84 * 1024) : S::kLds, stream, p);
     return hipGetLastError();
 }
 
 // Columns of the state that a workgroup of a walk holds (kDg: of a walk towards dg), and wavefronts it has.
 constexpr int linear_columns(int elem_bytes, bool dg, int Dv) { return elem_bytes == 2 && Dv > 64 ? 128 : 64; }
 constexpr int linear_waves(int elem_bytes, bool dg, int Dv) { return dg ? linear_columns(elem_bytes, dg, Dv) / 16 : 4; }
+
+// Floats of the state that a walk hands on (kDg: of both), its rows and columns rounded up to what a workgroup holds.
+constexpr int64_t linear_handed(int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
+{
+    const int64_t rows = Dk <= 32 ? 32 : Dk <= 64 ? 64 : Dk <= 128 ? 128 : 256, columns = linear_columns(elem_bytes, dg, (int)Dv);
+    return (dg ? 2 : 1) * rows * ((Dv + columns - 1) / columns * columns);
+}
 
 template <typename T, bool kOut, bool kDg>
 hipError_t launch_linear_walk(const LinearWalk<T>& p, hipStream_t stream);

@@ -476,3 +476,94 @@ def test_prefill_fork_decode_compact():
         n = whole[0].shape[1]
         over = np.abs(y[row, :last] - yr[0, -last:]) / (y_unit(dt, n, N, P) * ym[0, -last:])
         assert over.max() <= 1
+
+
+# ---- sizes at which rows are cut -------------------------------------------------------------------------
+
+# (batch, seqlen, nheads, headdim, dstate, ngroups, dtype): more walks than CUs, so that segments follow each other, with
+# one and several slices of columns, shared keys, both types; fewer, so that they walk at once
+CUT = [
+    (5, 2051, 56, 16, 32, 56, "bf16"), (2, 2100, 140, 32, 16, 70, "f32"), (1, 2049, 150, 144, 32, 150, "bf16"),
+    (300, 2048, 1, 16, 16, 1, "bf16"), (6, 2500, 100, 16, 16, 100, "bf16"), (2, 1500, 8, 32, 48, 4, "bf16"),
+]
+
+
+@pytest.mark.parametrize("c", CUT, ids=lambda c: "b{}_L{}_H{}_P{}_N{}_G{}_{}".format(*c))
+def test_cut_rows(c):
+    """Rows that are cut give what their heads give alone (one row and head, against the float64 recurrence, and every
+    head against a call with fewer, which is cut otherwise)."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, L, H, P, N, G, dt = c
+    gen = torch.Generator(device="cuda").manual_seed(500 + CUT.index(c))
+    T = torch.bfloat16 if dt == "bf16" else torch.float32
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")        # noqa: E731
+    v, k, q, dy = rand(b, L, G, P).to(T), rand(b, L, G, N).to(T), (rand(b, L, H, N) / N ** 0.5).to(T), rand(b, L, H, P).to(T)
+    g = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    init, dfinal = rand(b, H, P, N), rand(b, H, P, N)
+    y, fin = ssd.linear_forward(v, g, k, q, init)
+    out = ssd.linear_backward(v, g, k, q, dy, init, dfinal)
+    again = ssd.linear_backward(v, g, k, q, dy, init, dfinal)
+    assert all(torch.equal(out[n], again[n]) for n in out)
+    m = H // G
+    norm = lambda x, z: float((x.double() - z.double()).norm() / z.double().norm())        # noqa: E731
+    near, last = (5.2e-3 if dt == "bf16" else 2e-6), 6e-6        # twice what the header states of each
+    for i, j in ((0, 0), (b - 1, G - 1), (b // 2, G // 2)):
+        hs = slice(j * m, (j + 1) * m)
+        one = [t[i:i + 1, :, j:j + 1].contiguous() for t in (v, k)]
+        qs, ds = (t[i:i + 1, :, hs].contiguous() for t in (q, dy))
+        s0, s1 = (t[i:i + 1, hs].contiguous() for t in (init, dfinal))
+        yr, fr = ssd.linear_forward(one[0], g[hs].contiguous(), one[1], qs, s0)
+        assert norm(y[i:i + 1, :, hs], yr) <= near and norm(fin[i:i + 1, hs], fr) <= last
+        r = ssd.linear_backward(one[0], g[hs].contiguous(), one[1], qs, ds, s0, s1)
+        assert norm(out["dq"][i:i + 1, :, hs], r["dq"]) <= near and norm(out["dinit"][i:i + 1, hs], r["dinit"]) <= last
+        assert norm(out["dk"][i:i + 1, :, j:j + 1], r["dk"]) <= near and norm(out["dv"][i:i + 1, :, j:j + 1], r["dv"]) <= near
+    i, j = b - 1, G // 2
+    (yr, Sr), (ym, Sm) = ref.forward(*(f64(t.float())[i:i + 1, :, j:j + 1] if t is not g else f64(g)[j * m:j * m + 1]
+                                       for t in (v, g, k)), f64(q.float())[i:i + 1, :, j * m:j * m + 1],
+                                     f64(init)[i:i + 1, j * m:j * m + 1])
+    hold("y", y[i:i + 1, :, j * m:j * m + 1], yr, ym, y_unit(dt, L, N, P))
+    hold("final", fin[i:i + 1, j * m:j * m + 1], Sr, Sm, state_unit(dt, L, N, P))
+
+
+@pytest.mark.parametrize("lens", [[2500, 0, 1, 1024, 1025, 900, 30], [4000], [1024] * 9, [5] * 250 + [1500]],
+                         ids=["mixed", "one", "whole", "many"])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_varlen_in_chains(lens, dt):
+    """Packed rows whose segments follow each other: each as alone, and the same as in any other cut."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    n, T = len(lens), sum(lens)
+    H = -(-512 // n)
+    P, N = 16, 32
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    D = torch.bfloat16 if dt == "bf16" else torch.float32
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")        # noqa: E731
+    v, k, q = rand(T, H, P).to(D), rand(T, H, N).to(D), (rand(T, H, N) / N ** 0.5).to(D)
+    g = -torch.exp2(-8.0 * torch.arange(1, H + 1, device="cuda") / H)
+    h = rand(n, H, P, N)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+    y, fin = ssd.linear_forward_varlen(v, g, k, q, cu, h)
+    for i in sorted({0, 1, n // 2, n - 1} & set(range(n))):
+        a, z = int(cu[i]), int(cu[i + 1])
+        yr, fr = ssd.linear_forward(v[None, a:z], g, k[None, a:z], q[None, a:z], h[i:i + 1])
+        assert float((fin[i] - fr[0]).norm()) <= 6e-6 * float(fr.norm())
+        assert z == a or float((y[a:z].float() - yr[0].float()).norm()) <= (5.2e-3 if dt == "bf16" else 2e-6) * float(yr.float().norm())
+
+
+@pytest.mark.parametrize("cu", [[5, 2, 90, -7, 100000], [0, 3000, 0, 3000, 0], [2900, 60, 30, 0, -1]],
+                         ids=["jumps", "again", "falling"])
+def test_chain_with_bad_offsets_ends(cu):
+    """Offsets that overlap name more segments than there is room for: the call ends, inside its buffers."""
+    import torch
+    from test_gpu_guard import Guarded, _lib, _p, _stream
+    T, H, P, N = 3000, 128, 16, 16
+    d = ref.make(1, T, H, P, N, H, "bf16", False, seed=21)
+    v, g, k, q = (t[0] if t.dim() > 1 else t for t in inputs(d))
+    offsets = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    y, fin = Guarded((T, H, P), torch.bfloat16), Guarded((4, H, P, N), torch.float32)
+    ws = Guarded((_lib().ssd_linear_forward_varlen_workspace_bytes(T, 4, H, P, N, H, 1),), torch.uint8)
+    assert _lib().ssd_linear_forward_varlen(_p(v), _p(g), _p(k), _p(q), _p(offsets), 4, None, _p(y.t), _p(fin.t), T, H, P, N,
+                                            H, 1, _p(ws.t), ws.n, _stream()) == 0
+    torch.cuda.synchronize()
+    assert y.intact() and fin.intact() and ws.intact()
