@@ -310,6 +310,35 @@ template <int CH> struct LinearCols<float, CH> {
     __device__ __forceinline__ void load(Vec8<float>& f, int tile, int t) const { d.load(f, stage + tile, t); }
 };
 
+// An fp32 operand whose product keeps all of fp32: three bf16 values, hi + mid + lo, the value to 2^-24 (kThree), or a pair.
+template <typename T, bool kThree> struct LinearExact {
+    Pair<T> p;
+    Vec8<T> lo;
+    __device__ __forceinline__ void set(const float (&v)[8])
+    {
+        p.set(v);
+        if constexpr (kThree && sizeof(T) == 2) {
+            float left[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) left[i] = v[i] - p.hi.get(i) - p.lo.get(i);
+            pack8(lo, left);
+        }
+    }
+};
+// a exact and b in T, and the other way round
+template <typename T, bool kThree>
+__device__ __forceinline__ void mma_ex(f32x4& acc, const LinearExact<T, kThree>& a, const Vec8<T>& b)
+{
+    if constexpr (kThree && sizeof(T) == 2) mma(acc, a.lo, b);
+    mma_px(acc, a.p, b);
+}
+template <typename T, bool kThree>
+__device__ __forceinline__ void mma_xe(f32x4& acc, const Vec8<T>& a, const LinearExact<T, kThree>& b)
+{
+    if constexpr (kThree && sizeof(T) == 2) mma(acc, a, b.lo);
+    mma_xp(acc, a, b.p);
+}
+
 // the 4 values of a T quad at an LDS address, as floats
 __device__ __forceinline__ f32x4 lds_quad(unsigned a, bf16)
 {
@@ -711,16 +740,17 @@ void linear_walk_kernel(LinearWalk<T> p)
 #pragma unroll
                     for (int m = 0; m < 4; ++m) { s8[m] = st[2 * kb][j][m]; s8[4 + m] = st[2 * kb + 1][j][m]; }
                     if constexpr (kDg) {
-                        // dg is fp32 and takes its terms from here: pairs
-                        Pair<T> f, df;
+                        // dg is an fp32 sum in which much cancels, and takes its terms from here; most are S''s
+                        LinearExact<T, false> f;
+                        LinearExact<T, true> df;
                         f.set(s8);
 #pragma unroll
                         for (int m = 0; m < 4; ++m) { s8[m] = dst[2 * kb][j][m]; s8[4 + m] = dst[2 * kb + 1][j][m]; }
                         df.set(s8);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            mma_px(acc[t][j], f, qf[kb & 1][t]);
-                            mma_px(dacc[t][j], df, qf[kb & 1][t]);
+                            mma_ex(acc[t][j], f, qf[kb & 1][t]);
+                            mma_ex(dacc[t][j], df, qf[kb & 1][t]);
                         }
                     } else {
                         Vec8<T> f;
@@ -765,8 +795,11 @@ void linear_walk_kernel(LinearWalk<T> p)
             load_first();
         }
 
-        // the state behind the chunk: fp32 results, so the weighted values are pairs
-        Pair<T> vw[JT], dvw[kDg ? JT : 1];
+        // The state behind the chunk: fp32 results, so the weighted values are pairs.  Towards dg S takes three values, as S'
+        // does above: pairs left dg up to 3e-5 of its norm off where it cancels, these two leave 3e-6 (all four: 1e-6, and the
+        // backward 8 % longer instead of 5 %).
+        LinearExact<T, kDg> vw[JT];
+        LinearExact<T, false> dvw[kDg ? JT : 1];
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
             float w8[8];
@@ -791,8 +824,8 @@ void linear_walk_kernel(LinearWalk<T> p)
                 }
 #pragma unroll
                 for (int m = 0; m < 4; ++m) st[nt][j][m] = fmaf(st[nt][j][m], grow, st[nt][j][m]);
-                mma_xp(st[nt][j], kt[nt % kAheadK], vw[j]);
-                if constexpr (kDg) mma_xp(dst[nt][j], kt[nt % kAheadK], dvw[j]);
+                mma_xe(st[nt][j], kt[nt % kAheadK], vw[j]);
+                if constexpr (kDg) mma_xe(dst[nt][j], kt[nt % kAheadK], dvw[j]);
             }
             if (nt + kAheadK < kNT) colsk.load(kt[nt % kAheadK], S::kAtK, nt + kAheadK);
         }

@@ -91,7 +91,10 @@ hipError_t launch_state_move(float* states, const float* source, const int32_t* 
 {
     const int64_t strips = (slot_floats / 4 + 63) / 64 * nlayers;
     if (strips == 0 || nslots == 0) return hipSuccess;
-    const int64_t blocks = strips < 1024 ? strips : 1024;
+    // One workgroup to a CU where moves are few, with which starting it is most of its time (4 of 16 slots forked in 4 layers:
+    // 256 workgroups 9.9 us, the host's share; 512 14.8; 1024 24.4), two where a pool is large (180 of 256 states of
+    // 2.6 MB: 168, 164, 174).
+    const int64_t most = nslots <= 64 ? 256 : 512, blocks = strips < most ? strips : most;
     hipLaunchKernelGGL(state_move_kernel, dim3((unsigned)blocks), dim3(kWaves * 64), 0, stream, states,
                        source ? source : states, src, nlayers, (int)nslots, (int)nsource, slot_floats / 4);
     return hipGetLastError();

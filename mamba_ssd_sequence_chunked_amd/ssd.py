@@ -532,6 +532,11 @@ def delta_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, beta: torc
 
 # --- linear attention with a decay for each head, and pools of states --------------------------
 
+def _is(t, shape, dtype, index) -> bool:
+    """Whether t is what _need asks for, on GPU number index; without its messages, for the calls whose time is the host's."""
+    return t.dtype is dtype and t.shape == shape and t.get_device() == index and t.is_contiguous()
+
+
 def _linear_need(v, g, k, q, lead, H, P, N, G, dev):
     _need(v, "v", (*lead, G, P), v.dtype, dev)
     _need(g, "g", (H,), torch.float32, dev)
@@ -651,19 +656,24 @@ def linear_step(state: torch.Tensor, v: torch.Tensor, g: torch.Tensor, k: torch.
         raise ValueError("state must be (nslots, nheads, headdim, dstate) and v (batch, ngroups, headdim)")
     n, H, P, N = state.shape
     b, G = v.shape[0], v.shape[1]
-    dev = state.device
+    dev, T = state.device, v.dtype
+    i = state.get_device()
     code = _dtype_code(v)
-    _need(state, "state", (b if slots is None else n, H, P, N), torch.float32, dev)
-    _linear_need(v, g, k, q, (b,), H, P, N, G, dev)
-    if slots is not None:
-        _need(slots, "slots", (b,), torch.int32, dev)
+    f32 = torch.float32
+    if not (i >= 0 and _is(state, (b if slots is None else n, H, P, N), f32, i) and _is(v, (b, G, P), T, i)
+            and _is(g, (H,), f32, i) and _is(k, (b, G, N), T, i) and _is(q, (b, H, N), T, i)
+            and (slots is None or _is(slots, (b,), torch.int32, i)) and (y is None or _is(y, (b, H, P), T, i))):
+        _need(state, "state", (b if slots is None else n, H, P, N), f32, dev)
+        _linear_need(v, g, k, q, (b,), H, P, N, G, dev)
+        if slots is not None:
+            _need(slots, "slots", (b,), torch.int32, dev)
+        if y is not None:
+            _need(y, "y", (b, H, P), T, dev)
     if y is None:
-        y = torch.empty((b, H, P), dtype=v.dtype, device=dev)
-    else:
-        _need(y, "y", (b, H, P), v.dtype, dev)
+        y = torch.empty((b, H, P), dtype=T, device=dev)
     with _on_device(dev):
-        rc = lib.ssd_linear_step(_ptr(state), _ptr(slots), n, _ptr(v), _ptr(g), _ptr(k), _ptr(q), _ptr(y), b, H, P, N,
-                                 G, code, _stream(dev))
+        rc = lib.ssd_linear_step(state.data_ptr(), None if slots is None else slots.data_ptr(), n, v.data_ptr(),
+                                 g.data_ptr(), k.data_ptr(), q.data_ptr(), y.data_ptr(), b, H, P, N, G, code, _stream(dev))
     _check("ssd_linear_step", rc)
     return y
 
@@ -679,8 +689,10 @@ def state_move(states: torch.Tensor, src: torch.Tensor, source: Optional[torch.T
         raise ValueError("states must be ([nlayers,] nslots, nheads, headdim, dstate)")
     lead, n, one = states.shape[:-4], states.shape[-4], states.shape[-3:]
     dev = states.device
-    _need(states, "states", states.shape, torch.float32, dev)
-    _need(src, "src", (n,), torch.int32, dev)
+    i = states.get_device()
+    if not (i >= 0 and _is(states, states.shape, torch.float32, i) and _is(src, (n,), torch.int32, i)):
+        _need(states, "states", states.shape, torch.float32, dev)
+        _need(src, "src", (n,), torch.int32, dev)
     m = n
     if source is not None:
         if source.dim() != states.dim():
@@ -689,8 +701,8 @@ def state_move(states: torch.Tensor, src: torch.Tensor, source: Optional[torch.T
         _need(source, "source", (*lead, m, *one), torch.float32, dev)
     layers = lead[0] if lead else 1
     with _on_device(dev):
-        rc = lib.ssd_state_move(_ptr(states), _ptr(source), _ptr(src), layers, n, m, one[0] * one[1] * one[2],
-                                _stream(dev))
+        rc = lib.ssd_state_move(states.data_ptr(), None if source is None else source.data_ptr(), src.data_ptr(), layers,
+                                n, m, one[0] * one[1] * one[2], _stream(dev))
     _check("ssd_state_move", rc)
     return states
 
