@@ -156,8 +156,8 @@ hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states
 
 // A workgroup walks one slice of a row and head.  Measured with heads of 64 x 128 over 4096 tokens in bf16, where one row
 // alone takes a CU 175 us, two on one 332:
-//  - fewer walks than CUs: rows are cut into segments that walk at once, for a pass over K and V more (128 walks: 117 us,
-//    whole 139).
+//  - fewer walks than CUs: rows are cut into segments that walk at once, for a pass over K and V and two launches more, if
+//    that is less than a whole row's chunks take one after another (128 walks: 117 us, whole 139).
 //  - some more than CUs: a few CUs would have one more than the others from the first token to the last. In a chain
 //    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
 //    525, 558; backward of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
@@ -165,7 +165,8 @@ hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states
 //  - rows of different lengths: the same, in pieces of 1024 tokens (7 of 64 to 4096 tokens, 80 heads: 230 us, cut at
 //    once 346; 37 of up to 150, 16 heads of 128 x 128, 40 and 61). With few walks one long row would walk alone (256
 //    walks of up to 16384 tokens: 503 against 454), with many all CUs are busy in any case (2048 walks: 141, whole 128).
-Cut linear_cut(const DeltaDims& d, int64_t slices)
+constexpr double kStartsUs = 9;      // what two launches more take
+Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t least_chunks)
 {
     constexpr int64_t kCUs = 256, kLeast = 256;
     const int64_t walks = d.seqs * d.nheads * slices, over = walks % (2 * kCUs);
@@ -175,8 +176,9 @@ Cut linear_cut(const DeltaDims& d, int64_t slices)
         c.chain = walks >= 3 * kCUs / 2 && d.seqs <= kChainRows;
         c.seg = c.chain ? 1024 : std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
     } else if (walks < kCUs) {
-        const int64_t n = walks > 0 ? std::min<int64_t>(2 * kCUs / walks, d.seqlen / kLeast) : 1;
-        if (n <= 1) return c;
+        const int64_t chunks = (d.seqlen + kLC - 1) / kLC;
+        const int64_t n = walks > 0 ? std::min<int64_t>(2 * kCUs / walks, chunks / least_chunks) : 1;
+        if (n <= 2 || chunks * chunk_us * (n - 2) / n < kStartsUs) return c;
         c.seg = (d.seqlen + n - 1) / n;
     } else if (walks > kCUs && walks < 4 * kCUs && over > 0 && over <= 3 * kCUs / 2 && d.seqlen >= 8 * kLeast) {
         const int64_t n = walks < 11 * kCUs / 8 ? 3 : 2;
@@ -190,10 +192,13 @@ Cut linear_cut(const DeltaDims& d, int64_t slices)
     return c;
 }
 
-Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dv)
+// What a chunk takes a walk that runs alone: fp32's matrix products are a sixteenth of bf16's rate, and take it per 32
+// rows of the state.
+Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
     const int columns = linear_columns(elem_bytes, dg, (int)Dv);
-    return linear_cut(d, (Dv + columns - 1) / columns);
+    const double us = (elem_bytes == 2 ? 0.8 + Dk / 512. : 1 + Dk / 34.) * (dg ? 1.6 : 1);
+    return linear_cut(d, (Dv + columns - 1) / columns, us, elem_bytes == 2 ? 8 : 2);
 }
 
 struct GradLayout {
@@ -206,9 +211,9 @@ struct GradLayout {
 GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
 {
     GradLayout l;
-    l.cq = walk_cut(d, elem_bytes, true, d.dstate);
-    l.ck = walk_cut(d, elem_bytes, false, d.dstate);
-    l.cv = walk_cut(d, elem_bytes, false, d.headdim);
+    l.cq = walk_cut(d, elem_bytes, true, d.headdim, d.dstate);
+    l.ck = walk_cut(d, elem_bytes, false, d.headdim, d.dstate);
+    l.cv = walk_cut(d, elem_bytes, false, d.dstate, d.headdim);
     l.items = linear_items(d, l.cq.seg);
     const int columns = linear_columns(elem_bytes, true, (int)d.dstate);
     l.parts = (int)((d.dstate + columns - 1) / columns) * linear_waves(elem_bytes, true, (int)d.dstate);
@@ -227,7 +232,7 @@ GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
 
 size_t linear_forward_workspace(const DeltaDims& d, int elem_bytes)
 {
-    return 256 + walk_bytes(d, walk_cut(d, elem_bytes, false, d.headdim), elem_bytes, false, d.dstate, d.headdim);
+    return 256 + walk_bytes(d, walk_cut(d, elem_bytes, false, d.dstate, d.headdim), elem_bytes, false, d.dstate, d.headdim);
 }
 
 size_t linear_backward_workspace(const DeltaDims& d, int elem_bytes) { return grad_layout(d, elem_bytes).total; }
@@ -238,7 +243,7 @@ int64_t linear_blocks(const DeltaDims& d, int elem_bytes)
     for (const bool dg : {false, true})
         for (const int64_t Dv : {d.headdim, d.dstate}) {
             const int columns = linear_columns(elem_bytes, dg, (int)Dv);
-            most = std::max(most, linear_items(d, walk_cut(d, elem_bytes, dg, Dv).seg) * d.nheads * ((Dv + columns - 1) / columns) *
+            most = std::max(most, linear_items(d, walk_cut(d, elem_bytes, dg, d.headdim + d.dstate - Dv, Dv).seg) * d.nheads * ((Dv + columns - 1) / columns) *
                                       (linear_waves(elem_bytes, dg, (int)Dv) > 4 ? 2 : 1));
         }
     return most;
@@ -261,7 +266,7 @@ hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T
     p.Dk = (int)d.dstate;
     p.Dv = (int)d.headdim;
     p.d = d;
-    return walk<T, false>(p, walk_cut(d, sizeof(T), false, d.headdim), init, static_cast<float*>(workspace), stream);
+    return walk<T, false>(p, walk_cut(d, sizeof(T), false, d.dstate, d.headdim), init, static_cast<float*>(workspace), stream);
 }
 
 template <typename T>
