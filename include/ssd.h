@@ -396,14 +396,14 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  * q is a head's own; head h reads k and v of group h / (nheads / ngroups), ngroups = nheads where nothing is shared.
  * Conventions and errors are those at the top of this header, and:
  *   - g float (nheads) is the log decay, <= 0 and constant in time; it is not clamped, except that every g below
- *     -1000 acts as -1000 (exp is 0 in fp32 from -104 on), so -inf leaves each token alone. g = 0 is plain causal
+ *     -1000 acts as -1000, so -inf leaves each token alone. A power of the decay below 2^-126 (exp(-87)) is 0. g = 0 is plain causal
  *     linear attention. No scale is applied to q.
  *   - headdim and dstate are multiples of 16 in [16, 256]; nheads * headdim and nheads * dstate <= 2^20; 0 <= batch <=
  *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
  *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate
  *     < 2^34, tokens * ngroups * the wider < 2^34; for ssd_linear_step batch * nheads * headdim < 2^28.
- *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (1e-6 to 3e-6 of their norm): what leads to
- *     them is carried as pairs of bf16 values. bf16 outputs are a little further off than their own rounding (1.7e-3 of the
+ *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (5e-7 of their norm, dg 4e-6 where its terms
+ *     cancel): what leads to them is carried as two or three bf16 values. bf16 outputs are a little further off than their own rounding (1.7e-3 of the
  *     norm), because the scores and, where they are read, the states are rounded to bf16 on the way: up to 2.6e-3.
  *     With fp32 inputs everything is fp32.
  *   - Sums are made in a fixed order: the same call gives the same bits.
@@ -445,7 +445,7 @@ int ssd_linear_forward_varlen(const void* v, const float* g, const void* k, cons
 /* Gradients of ssd_linear_forward for dL/dy = dy and dL/d(final_states) = dfinal (NULL = 0).
  *   dy T like y; dfinal float (batch, nheads, headdim, dstate) or NULL
  *   dv, dk T like v, k: summed over the heads of a group, in their order, and rounded once; dq T like q
- *   dg float (nheads): summed over tokens and batch rows, 0 where g is below -104 (and without rows)
+ *   dg float (nheads): summed over tokens and batch rows, 0 where g is below -87.3 (and without rows)
  *   dinit float (batch, nheads, headdim, dstate), written also when init_states is NULL
  *   workspace of at least ssd_linear_backward_workspace_bytes() bytes: with shared keys and values an fp32 copy of every
  *     head's dk and dv, else the states between segments and a few sums */

@@ -36,6 +36,8 @@ __global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ lo
     }
     const int64_t count = max((n + seg - 1) / seg, (int64_t)1);
     const float gl = fmaxf(g[h], -1000.f);
+    LinearDecay decay;
+    decay.set(gl, (int)min(seg, n));
     f32x4 s = {0.f, 0.f, 0.f, 0.f}, ds = {0.f, 0.f, 0.f, 0.f};
     if (init) s = *reinterpret_cast<const f32x4*>(init + rh * PN + at);
     for (int64_t c = 0; c < count; ++c) {
@@ -48,14 +50,13 @@ __global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ lo
         }
         *reinterpret_cast<f32x4*>(loc + to) = s;
         if constexpr (kDg) *reinterpret_cast<f32x4*>(dloc + to) = ds;
-        const float grow = expm1f(gl * (float)len);
+        const float a = len == min(seg, n) ? decay.next() : expf(gl * (float)len);
 #pragma unroll
         for (int m = 0; m < 4; ++m) {
             if constexpr (kDg) {
-                const float both = fmaf((float)len, s[m], ds[m]);
-                ds[m] = fmaf(both, grow, both) + dadd[m];
+                ds[m] = fmaf(fmaf((float)len, s[m], ds[m]), a, dadd[m]);
             }
-            s[m] = fmaf(s[m], grow, s[m]) + add[m];
+            s[m] = fmaf(s[m], a, add[m]);
         }
     }
 }

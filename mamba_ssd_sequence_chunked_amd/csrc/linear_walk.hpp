@@ -169,6 +169,30 @@ __device__ __forceinline__ bool linear_task(const DeltaDims& d, int64_t seg, int
     }
 }
 
+// A power a^n that a state is multiplied by again and again.  Rounded to fp32 it would be off by the same part every
+// time, which adds up where the decay is slow; so the fp32 neighbours below and above it take turns such that their
+// product stays within one rounding of the power's.
+struct LinearDecay {
+    float low, high, share, sum;             // share: of the turns that are high's
+    __device__ __forceinline__ void set(float g, int n)
+    {
+        const double exact = exp((double)g * n);
+        low = (float)exact;
+        if (low > exact) low = __uint_as_float(__float_as_uint(low) - 1);
+        if (exact < 1.1754943508222875e-38) low = 0.f;
+        high = low > 0.f ? __uint_as_float(__float_as_uint(low) + 1) : 0.f;
+        share = low > 0.f ? (float)((exact - low) / ((double)high - low)) : 0.f;
+        sum = 0.5f;
+    }
+    __device__ __forceinline__ float next()
+    {
+        sum += share;
+        const bool up = sum >= 1.f;
+        sum = up ? sum - 1.f : sum;
+        return up ? high : low;
+    }
+};
+
 // ---- copies ---------------------------------------------------------------------------------------------
 
 // One wavefront's share of the copies of a tile of 32 rows: row r from base + r * row_bytes (back: (31 - r) *
@@ -434,6 +458,16 @@ void linear_walk_kernel(LinearWalk<T> p)
     const int col0 = slice * NW * JT * 16;
     const int validk = p.Dk * S::kEs / 16, validv = min(CHv, (p.Dv - col0) * S::kEs / 16);
     const float gl = fmaxf(p.g[h], -1000.f);
+    if constexpr (!kOut) {
+        // What a token adds to the state n tokens later is 0 in fp32 where a^n is below e^-200, whatever finite values it
+        // has (their product is below e^89, and 0 begins at e^-103): the walk starts where something is left.
+        const float reach = -200.f / gl;
+        if (gl < 0.f && reach < (float)it.len) {
+            const int skip = (it.len - 1 - (int)reach) / kLC * kLC;
+            it.len -= skip;
+            if (!p.back) it.start += skip;
+        }
+    }
 
     // sources: the head's first column, the walk's first token; from there 32 tokens on with every chunk
     const char* src[4];
@@ -492,11 +526,11 @@ void linear_walk_kernel(LinearWalk<T> p)
         tiled[m] = gap > 0 ? tilew[m] * gap : 0.f;
     }
     float outw[8];
-    float grow;                                                   // a^32 - 1: the state's own share stays exact
+    LinearDecay decay;
+    decay.set(gl, kLC);
     auto weights = [&](int rows) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) outw[i] = expf(gl * max(rows - ((i >> 2) * 16 + 4 * g4 + (i & 3)) - e, 0));
-        grow = expm1f(gl * rows);
     };
     weights(kLC);
 
@@ -795,10 +829,11 @@ void linear_walk_kernel(LinearWalk<T> p)
             load_first();
         }
 
-        // The state behind the chunk: fp32 results, so the weighted values are pairs.  Towards dg S takes three values, as S'
-        // does above: pairs left dg up to 3e-5 of its norm off where it cancels, these two leave 3e-6 (all four: 1e-6, and the
-        // backward 8 % longer instead of 5 %).
-        LinearExact<T, kDg> vw[JT];
+        // The state behind the chunk is an fp32 result: its weighted values are three bf16 values each, the state then as exact as
+        // fp32 sums are (1e-7 to 4e-7 of its norm).  Pairs left 2.4e-6, and where dg cancels up to 3e-5 of that; they take
+        // 2 % off the forward of 320 rows, 10 % off 65536 tokens' with 256 rows of state.  S' adds to dg's terms what
+        // a chunk itself brings, a small part: pairs (dg's error at most 3e-6; with three 1e-6, the backward 3 % longer).
+        LinearExact<T, true> vw[JT];
         LinearExact<T, false> dvw[kDg ? JT : 1];
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
@@ -813,17 +848,16 @@ void linear_walk_kernel(LinearWalk<T> p)
                 dvw[j].set(w8);
             }
         }
+        const float a = rows < kLC ? expf(gl * rows) : decay.next();
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
             for (int j = 0; j < JT; ++j) {
                 if constexpr (kDg) {
-                    const f32x4 both = dst[nt][j] + (float)rows * st[nt][j];
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) dst[nt][j][m] = fmaf(both[m], grow, both[m]);
+                    for (int m = 0; m < 4; ++m) dst[nt][j][m] = fmaf((float)rows, st[nt][j][m], dst[nt][j][m]) * a;
                 }
-#pragma unroll
-                for (int m = 0; m < 4; ++m) st[nt][j][m] = fmaf(st[nt][j][m], grow, st[nt][j][m]);
+                st[nt][j] *= a;
                 mma_xe(st[nt][j], kt[nt % kAheadK], vw[j]);
                 if constexpr (kDg) mma_xe(dst[nt][j], kt[nt % kAheadK], dvw[j]);
             }

@@ -1,0 +1,250 @@
+"""Calls of linear attention and of state_move that their documentation allows: guard bands around every output and the
+workspace, captured and replayed calls, two streams at once, one tensor in two places, a workspace kept by the caller,
+offsets past 32 bits, and the views that are refused."""
+import numpy as np
+import pytest
+
+import linear_ref as ref
+from test_gpu_delta_guard import call, typed
+from test_gpu_guard import Guarded, _code, _lib, _p, _stream
+from test_gpu_linear import check, dev, f64, inputs
+
+pytestmark = pytest.mark.gpu
+
+# (batch, seqlen, nheads, headdim, dstate, ngroups, dtype, init): odd sizes, cut rows, shared keys, wide rows
+SHAPES = [
+    (2, 77, 6, 64, 128, 2, "bf16", True), (1, 33, 5, 16, 48, 1, "f32", False), (3, 129, 3, 80, 80, 3, "bf16", False),
+    (1, 95, 2, 256, 256, 1, "f32", True), (1, 700, 2, 144, 240, 2, "bf16", True), (1, 31, 270, 64, 128, 5, "bf16", False),
+    (2, 2049, 150, 16, 16, 150, "bf16", True), (1, 300, 3, 32, 16, 3, "f32", True),
+]
+IDS = ["b{}_L{}_H{}_P{}_N{}_G{}_{}_i{}".format(*c) for c in SHAPES]
+
+
+def make(c, seed):
+    b, L, H, P, N, G, dt, init = c
+    return ref.make(b, L, H, P, N, G, dt, init, seed=seed + SHAPES.index(c))
+
+
+@pytest.mark.parametrize("c", SHAPES, ids=IDS)
+def test_forward_and_varlen_guards(c):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, L, H, P, N, G, dt, init = c
+    d = make(c, 700)
+    (v, g, k, q), h, lib, code = inputs(d), dev(d["init"]), _lib(), _code(dt)
+    y, fin = Guarded((b, L, H, P), typed(dt)), Guarded((b, H, P, N), torch.float32)
+    ws = Guarded((lib.ssd_linear_forward_workspace_bytes(b, L, H, P, N, G, code),), torch.uint8)
+    call("ssd_linear_forward", [v, g, k, q, h], [y, fin], ws, [b, L, H, P, N, G, code])
+    yr, fr = ssd.linear_forward(v, g, k, q, h)
+    assert torch.equal(y.t, yr) and torch.equal(fin.t, fr)
+
+    # one long sequence, an empty one and the rest
+    cut = L // 2 + 1
+    cu = torch.tensor([0, cut, cut, b * L], dtype=torch.int32, device="cuda")
+    vf, kf, qf = (t.reshape(b * L, *t.shape[2:]) for t in (v, k, q))
+    y, fin = Guarded((b * L, H, P), typed(dt)), Guarded((3, H, P, N), torch.float32)
+    ws = Guarded((lib.ssd_linear_forward_varlen_workspace_bytes(b * L, 3, H, P, N, G, code),), torch.uint8)
+    call("ssd_linear_forward_varlen", [vf, g, kf, qf, cu, 3, None], [y, fin], ws, [b * L, H, P, N, G, code])
+    yr, fr = ssd.linear_forward_varlen(vf, g, kf, qf, cu)
+    assert torch.equal(y.t, yr) and torch.equal(fin.t, fr)
+
+
+@pytest.mark.parametrize("c", SHAPES, ids=IDS)
+def test_backward_guards(c):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, L, H, P, N, G, dt, init = c
+    d = make(c, 720)
+    (v, g, k, q), h, dy, df, T = inputs(d), dev(d["init"]), dev(d["dy"], dt), dev(d["dfinal"]), typed(dt)
+    outs = dict(dv=Guarded(v.shape, T), dg=Guarded((H,), torch.float32), dk=Guarded(k.shape, T), dq=Guarded(q.shape, T),
+                dinit=Guarded((b, H, P, N), torch.float32))
+    ws = Guarded((_lib().ssd_linear_backward_workspace_bytes(b, L, H, P, N, G, _code(dt)),), torch.uint8)
+    call("ssd_linear_backward", [v, g, k, q, h, dy, df], list(outs.values()), ws, [b, L, H, P, N, G, _code(dt)])
+    want = ssd.linear_backward(v, g, k, q, dy, h, df)
+    assert all(torch.equal(outs[n].t, want[n]) for n in want)
+
+
+@pytest.mark.parametrize("b,H,P,N,G,dt", [(3, 5, 48, 80, 5, "bf16"), (1, 2, 256, 256, 1, "f32"), (9, 3, 16, 16, 3, "bf16")])
+def test_step_and_move_guards(b, H, P, N, G, dt):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(b, 1, H, P, N, G, dt, True, seed=740)
+    v, g, k, q = (t[:, 0].contiguous() if t.dim() > 1 else t for t in inputs(d))
+    n = b + 2
+    pool, y = Guarded((n, H, P, N), torch.float32), Guarded((b, H, P), typed(dt))
+    start = torch.randn((n, H, P, N), device="cuda")
+    pool.t.copy_(start)
+    slots = torch.tensor([(i * 2) % n if i != 1 else -1 for i in range(b)], dtype=torch.int32, device="cuda")
+    torch.cuda.synchronize()
+    assert _lib().ssd_linear_step(_p(pool.t), _p(slots), n, _p(v), _p(g), _p(k), _p(q), _p(y.t), b, H, P, N, G, _code(dt),
+                                  _stream()) == 0
+    torch.cuda.synchronize()
+    assert pool.intact() and y.intact()
+    other = start.clone()
+    assert torch.equal(ssd.linear_step(other, v, g, k, q, slots=slots), y.t) and torch.equal(other, pool.t)
+    src = torch.arange(n - 1, -1, -1, dtype=torch.int32, device="cuda")
+    src[0] = -1
+    assert _lib().ssd_state_move(_p(pool.t), None, _p(src), 1, n, n, H * P * N, _stream()) == 0
+    torch.cuda.synchronize()
+    assert pool.intact() and torch.equal(pool.t[1:], other.flip(0)[1:]) and not pool.t[0].any()
+
+
+def test_captured_and_replayed():
+    """A forward whose rows are a chain, one that is cut at once, a packed batch with other offsets, and decoding with
+    reordering, in one graph; replayed on new inputs with eager work between."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    P, N = 16, 32
+    shapes = [(2, 2050, 150), (1, 1400, 4)]
+    data = [[t for t in inputs(ref.make(b, L, H, P, N, H, "bf16", False, seed=760))] for b, L, H in shapes]
+    T, H = 260, 4
+    vl = [t[0] if t.dim() > 1 else t for t in inputs(ref.make(1, T, H, P, N, H, "bf16", False, seed=761))]
+    cu = torch.tensor([0, 65, 130, 195, T], dtype=torch.int32, device="cuda")
+    pool = torch.zeros((6, H, P, N), device="cuda")
+    into = torch.tensor([0, 1, 2, 3, -1, -1], dtype=torch.int32, device="cuda")
+    src = torch.tensor([1, 0, 2, 2, 3, -1], dtype=torch.int32, device="cuda")
+    slots = torch.tensor([0, 3, 4, -1], dtype=torch.int32, device="cuda")
+    tok = [t[:4].contiguous() if t.dim() > 1 else t for t in vl]
+
+    def run():
+        out = [ssd.linear_forward(*x) for x in data]
+        back = ssd.linear_backward(*data[0], data[0][0])
+        y, fin = ssd.linear_forward_varlen(vl[0], vl[1], vl[2], vl[3], cu)
+        ssd.state_move(pool, into, source=fin)
+        ssd.state_move(pool, src)
+        return [t for o in out for t in o] + list(back.values()) + [y, fin, ssd.linear_step(pool, *tok, slots=slots), pool]
+
+    run()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = run()
+    for n, offsets in enumerate(([0, 1, 2, 3, T], [0, 0, 200, 200, T], [0, 33, 97, 259, T])):
+        for x in data:
+            x[0].copy_(torch.randn(x[0].shape, device="cuda"))
+        cu.copy_(torch.tensor(offsets, dtype=torch.int32))
+        want = [t.clone() for t in run()]
+        torch.cuda.synchronize()
+        print("replay", n, flush=True)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+def test_two_streams_at_once():
+    """Chains on two streams: each has its own workspace and counters."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    P, N, H = 16, 32, 160
+    xs = [inputs(ref.make(2, 2048 + 7 * s, H, P, N, H, "bf16", False, seed=770 + s)) for s in range(2)]
+    want = [ssd.linear_forward(*x) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = [[], []]
+    for _ in range(3):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(ssd.linear_forward(*xs[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(a, b) for g in got[i] for a, b in zip(g, want[i]))
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_one_tensor_in_two_places(dt):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(2, 70, 4, 64, 64, 4, dt, True, seed=780)
+    v, g, k, _ = inputs(d)
+    h = dev(d["init"])
+    a, b = ssd.linear_forward(k, g, k, k, h), ssd.linear_forward(k, g, k.clone(), k.clone(), h)
+    assert all(torch.equal(s, t) for s, t in zip(a, b))
+    a = ssd.linear_backward(v, g, k, k, v, h, h)
+    b = ssd.linear_backward(v, g, k, k.clone(), v.clone(), h, h.clone())
+    assert all(torch.equal(a[n], b[n]) for n in a)
+
+
+def test_workspace_of_the_callers():
+    """Kept between calls of different sizes and cuts, with whatever the last call left in it; one too small is refused."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    lib = ssd.load_library()
+    sizes = [(2, 2050, 150), (1, 1500, 4), (2, 2050, 150), (300, 10, 1)]
+    need = [lib.ssd_linear_forward_workspace_bytes(b, L, H, 16, 32, H, ssd.SSD_BF16) for b, L, H in sizes]
+    ws = torch.full((max(need),), 0xa5, dtype=torch.uint8, device="cuda")
+    for b, L, H in sizes:
+        x = inputs(ref.make(b, L, H, 16, 32, H, "bf16", False, seed=790))
+        r, s = ssd.linear_forward(*x, workspace=ws), ssd.linear_forward(*x)
+        assert torch.equal(r[0], s[0]) and torch.equal(r[1], s[1])
+    x = inputs(ref.make(*sizes[0], 16, 32, sizes[0][2], "bf16", False, seed=790))
+    with pytest.raises(ssd.SSDError):
+        ssd.linear_forward(*x, workspace=ws[:need[0] - 1])
+
+
+def test_padding_leaves_the_rest():
+    """Rows of one batch with tokens behind their end that hold zeros: their outputs up to there are those of their own
+    length, and their final states decay on."""
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(3, 90, 4, 32, 48, 2, "bf16", True, seed=795)
+    ends = (90, 41, 0)
+    for row, n in enumerate(ends):
+        for t in ("v", "k", "q"):
+            d[t][row, n:] = 0.0
+    y, fin = ssd.linear_forward(*inputs(d), dev(d["init"]))
+    check(y, fin, ref.forward(d["v"], d["g"], d["k"], d["q"], d["init"]), "bf16", 90, 48, 32)
+    assert not y[2].any()
+
+
+def test_offsets_past_32_bits():
+    """More than 2^32 bytes of q, y and a pool: the last tokens and slots are those of a call on them alone."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, L, H, P, N = 1, 41000, 256, 16, 256
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn((b, L, H, N), generator=gen, device="cuda", dtype=torch.bfloat16)
+    k, v = (torch.randn((b, L, 1, w), generator=gen, device="cuda", dtype=torch.bfloat16) for w in (N, P))
+    assert q.numel() * 2 > 2 ** 32
+    g = torch.full((H,), -7.0, device="cuda")                # 200 tokens back nothing is left
+    y, fin = ssd.linear_forward(v, g, k, q)
+    yt, ft = ssd.linear_forward(*(t if t is g else t[:, -256:].contiguous() for t in (v, g, k, q)))
+    assert torch.equal(y[:, -128:], yt[:, -128:]) or (y[:, -128:].float() - yt[:, -128:].float()).norm() <= 5.2e-3 * yt[:, -128:].float().norm()
+    assert (fin - ft).norm() <= 1e-6 * ft.norm()
+    del q, y, k, v
+    pool = torch.zeros((34000, 8, 64, 64), device="cuda")    # 4.5 GB
+    assert pool.numel() * 4 > 2 ** 32
+    src = torch.full((34000,), -2, dtype=torch.int32, device="cuda")
+    one = torch.randn((2, 8, 64, 64), generator=gen, device="cuda")
+    src[33999], src[0], src[16500] = 1, 0, 1
+    ssd.state_move(pool, src, source=one)
+    assert torch.equal(pool[33999], one[1]) and torch.equal(pool[0], one[0]) and torch.equal(pool[16500], one[1])
+    assert not pool[1:16500].any() and not pool[16501:33999].any()
+    v, k = torch.randn((1, 8, 64), device="cuda"), torch.randn((1, 8, 64), device="cuda")
+    state = one[1:2].clone()
+    want = ssd.linear_step(state, v, g[:8].contiguous(), k, k)
+    got = ssd.linear_step(pool, v, g[:8].contiguous(), k, k, slots=torch.tensor([33999], dtype=torch.int32, device="cuda"))
+    assert torch.equal(got, want) and torch.equal(pool[33999], state[0])
+
+
+def test_views_that_are_refused():
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(2, 40, 4, 32, 64, 2, "f32", True, seed=798)
+    v, g, k, q = inputs(d)
+    with pytest.raises(ValueError):                          # strided: every second token
+        ssd.linear_forward(v[:, ::2], g, k[:, ::2], q[:, ::2])
+    flat = torch.empty(v.numel() + 1, device="cuda")
+    off = flat[1:].view(v.shape)                             # 4 bytes off
+    off.copy_(v)
+    with pytest.raises(ssd.SSDError):
+        ssd.linear_forward(off, g, k, q)
+    pool = torch.zeros((4, 4, 32, 64), device="cuda")
+    rows = [t[:, 0].contiguous() for t in (v, k, q)]
+    with pytest.raises(ValueError):                          # slots in 64 bits
+        ssd.linear_step(pool, rows[0], g, rows[1], rows[2], slots=torch.tensor([0, 1], device="cuda"))
+    with pytest.raises(ValueError):                          # a view of every second slot
+        ssd.state_move(torch.zeros((8, 4, 32, 64), device="cuda")[::2], torch.zeros(4, dtype=torch.int32, device="cuda"))
+    with pytest.raises(ssd.SSDError):                        # a pool moved into itself by name
+        ssd.state_move(pool, torch.zeros(4, dtype=torch.int32, device="cuda"), source=pool)
+    with pytest.raises(ssd.SSDError):                        # y in the states
+        ssd.linear_step(pool, rows[0], g, rows[1], rows[2], slots=torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
+                        y=pool.view(-1)[:256].view(2, 4, 32))
