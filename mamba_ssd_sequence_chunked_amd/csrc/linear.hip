@@ -163,18 +163,22 @@ hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states
 //    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
 //    525, 558; backward of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
 //    the starts are worth.
-//  - rows of different lengths: the same, in pieces of 1024 tokens (7 of 64 to 4096 tokens, 80 heads: 230 us, cut at
-//    once 346; 37 of up to 150, 16 heads of 128 x 128, 40 and 61). With few walks one long row would walk alone (256
-//    walks of up to 16384 tokens: 503 against 454), with many all CUs are busy in any case (2048 walks: 141, whole 128).
+//  - rows of different lengths: the same, in pieces of 1024 tokens (20 of up to 1000, 13 heads of 128 x 128: 59 us, cut at
+//    once 102; 7 of 64 to 4096, 80 heads: 230, 346; only 336 walks of 4096 tokens and 256 rows of state are slower, 318, 286).
+//    Whole where they are short, 384 tokens on average: a chain's workgroups have a CU each, and so little to walk is
+//    mostly waiting for a first chunk, which two on a CU share (37 of up to 150, 16 heads of 128 x 128: 34 us, in a chain
+//    45; averages of 300 70, 78; of 500 111, 105). In fp32, where one fills a CU, 192 (400 walks of 150 on average: 72, 81; of
+//    300 166, 147). With many walks all CUs are busy in any case (2048: 141, whole 128).
+//    Few walks are cut at once, since one long row would walk alone, but into three at least, as above.
 constexpr double kStartsUs = 9;      // what two launches more take
-Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t least_chunks)
+Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t least_chunks, int64_t brief)
 {
     constexpr int64_t kCUs = 256, kLeast = 256;
     const int64_t walks = d.seqs * d.nheads * slices, over = walks % (2 * kCUs);
     Cut c{kWholeRows, false};
     if (d.cu) {
-        if (walks >= 4 * kCUs) return c;
-        c.chain = walks >= 3 * kCUs / 2 && d.seqs <= kChainRows;
+        if (walks >= 4 * kCUs || (d.tokens <= brief * d.seqs && walks > kCUs)) return c;
+        c.chain = walks > kCUs && d.seqs <= kChainRows;
         c.seg = c.chain ? 1024 : std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
     } else if (walks < kCUs) {
         const int64_t chunks = (d.seqlen + kLC - 1) / kLC;
@@ -189,7 +193,7 @@ Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t leas
         return c;
     }
     c.seg = (c.seg + 63) / 64 * 64;
-    if ((d.cu ? d.tokens : d.seqlen) <= c.seg) return Cut{kWholeRows, false};
+    if (d.cu ? d.tokens <= (c.chain ? 1 : 2) * c.seg : d.seqlen <= c.seg) return Cut{kWholeRows, false};
     return c;
 }
 
@@ -199,7 +203,7 @@ Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv
 {
     const int columns = linear_columns(elem_bytes, dg, (int)Dv);
     const double us = (elem_bytes == 2 ? 0.8 + Dk / 512. : 1 + Dk / 34.) * (dg ? 1.6 : 1);
-    return linear_cut(d, (Dv + columns - 1) / columns, us, elem_bytes == 2 ? 8 : 2);
+    return linear_cut(d, (Dv + columns - 1) / columns, us, elem_bytes == 2 ? 8 : 2, elem_bytes == 2 ? 384 : 192);
 }
 
 struct GradLayout {

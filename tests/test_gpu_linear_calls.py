@@ -248,3 +248,49 @@ def test_views_that_are_refused():
     with pytest.raises(ssd.SSDError):                        # y in the states
         ssd.linear_step(pool, rows[0], g, rows[1], rows[2], slots=torch.tensor([0, 1], dtype=torch.int32, device="cuda"),
                         y=pool.view(-1)[:256].view(2, 4, 32))
+
+
+def packed(lens, H, P, N, dt, seed):
+    """Inputs of a packed batch, and its offsets."""
+    import torch
+    v, g, k, q = inputs(ref.make(1, sum(lens), H, P, N, H, dt, False, seed=seed))
+    return v[0], g, k[0], q[0], torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("lens,H", [([1700] * 30 + [1] * 95 + [0] * 5 + [1650] * 30 + [40] * 95, 2), ([33] * 40, 16), ([400, 370] * 5, 30),
+                                    ([2000, 40, 1100], 3), ([700, 300], 3), ([31] * 300, 4)],
+                         ids=["chain255", "short", "chain", "cut", "whole", "many"])
+def test_packed_rows_alone(lens, H):
+    """Rows of a packed batch, run whole, cut at once and in chains, against each row by itself."""
+    import mamba_ssd_sequence_chunked_amd as ssd
+    P = N = 16
+    v, g, k, q, cu = packed(lens, H, P, N, "f32", 800)
+    y, fin = ssd.linear_forward_varlen(v, g, k, q, cu)
+    ends = np.cumsum([0] + lens)
+    for i in sorted(set(range(0, len(lens), max(1, len(lens) // 12))) | {len(lens) - 1}):
+        at = slice(ends[i], ends[i + 1])
+        a, b = ssd.linear_forward(v[None, at].contiguous(), g, k[None, at].contiguous(), q[None, at].contiguous())
+        # fp32 on both sides: 33 roundings of 2^-24 a chunk, in at most 54 chunks, of random signs
+        limit = 2 * 2.0 ** -24 * (33 * 54) ** 0.5
+        assert (y[at] - a[0]).norm() <= limit * a.norm() and (fin[i] - b[0]).norm() <= limit * b.norm()
+
+
+@pytest.mark.parametrize("H,T", [(60, 5000), (3, 2600), (150, 700)])
+def test_captured_packed_with_other_offsets(H, T):
+    """A chain, rows cut at once, and whole ones, captured with one set of offsets and replayed with others."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    v, g, k, q, cu = packed([T // 5] * 5, H, 16, 32, "bf16", 810)
+    ssd.linear_forward_varlen(v, g, k, q, cu)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = ssd.linear_forward_varlen(v, g, k, q, cu)
+    for offsets in ([0, T, T, T, T, T], [0, 1, 2, 3, 4, T], [0, 0, 0, T // 2, T, T], [0, T // 3, T // 3, T // 2, T - 1, T]):
+        cu.copy_(torch.tensor(offsets, dtype=torch.int32))
+        q.normal_()
+        want = ssd.linear_forward_varlen(v, g, k, q, cu)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
