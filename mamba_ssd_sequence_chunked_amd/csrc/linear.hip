@@ -1,10 +1,11 @@
 // linear.hip - linear attention with a decay for each head: the forward and the backward as walks (linear_walk.hpp), and
 // the small kernels between and behind them.
 //
-// The forward is one walk.  The backward is three: dq forwards, with the sums of dg; dk and dv backwards.  Where there are
-// fewer walks than the GPU holds, rows are cut into segments: a first pass leaves what every segment but the last adds to
-// the state, linear_join_kernel turns that into the states that enter them, and the walk runs over all segments
-// at once.  Where there are a few too many, segments follow each other in a chain (see linear_cut).
+// The forward is one walk.  The backward is three: dq forwards, with the sums of dg; dk and dv backwards, both in one
+// launch.  Where there are fewer walks than the GPU holds, rows are cut into segments: a first pass leaves what
+// every segment but the last adds to the state, linear_join_kernel turns that into the states that enter them, and the
+// walk runs over all segments at once.  Where there are a few too many, segments follow each other in a chain (see
+// linear_cut).
 #include <algorithm>
 
 #include "linear_walk.hpp"
@@ -13,14 +14,16 @@ namespace ssd {
 
 namespace {
 
-// What enters every segment, from what each adds (loc, in place; with dloc the derivative for g too).  A thread
-// has 4 elements of a row and head and goes along the row.
+// What enters every segment, from what each adds (loc, in place; with dloc the derivative for g too; loc2 where two
+// walks are joined).  A thread has 4 elements of a row and head and goes along the row.
 //   S_0 = init;  S_{i+1} = a^len S_i + loc_i;   S'_0 = 0;  S'_{i+1} = a^len (S'_i + len S_i) + dloc_i
 template <bool kDg>
-__global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ loc, float* __restrict__ dloc,
-                                                          const float* __restrict__ init, const float* __restrict__ g,
-                                                          DeltaDims d, int64_t seg, bool back, int64_t PN)
+__global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ loc, float* __restrict__ loc2,
+                                                          float* __restrict__ dloc, const float* __restrict__ init,
+                                                          const float* __restrict__ g, DeltaDims d, int64_t seg,
+                                                          bool back, int64_t PN)
 {
+    if (blockIdx.y > 0) loc = loc2;
     const int64_t quads = PN / 4;
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i >= d.seqs * d.nheads * quads) return;
@@ -105,10 +108,11 @@ struct Cut {
     bool chain;
 };
 
-__global__ __launch_bounds__(256) void linear_zero_kernel(unsigned* p, int64_t n)
+__global__ __launch_bounds__(256) void linear_zero_kernel(unsigned* p, int64_t n, unsigned* p2, int64_t n2)
 {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) p[i] = 0;
+    else if (i - n < n2) p2[i - n] = 0;
 }
 
 // Bytes of workspace for one walk: the items' states (dg: twice that), or a chain's counters and states.
@@ -120,39 +124,59 @@ size_t walk_bytes(const DeltaDims& d, const Cut& c, int elem_bytes, bool dg, int
     return (dg ? 2 : 1) * bytes_up(state_floats(d, linear_items(d, c.seg)));
 }
 
-// The walk, or where rows are cut its steps.
-template <typename T, bool kDg>
-hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states, hipStream_t stream)
+template <bool kOut, bool kDg, typename T> hipError_t launch(LinearWalk<T> (&p)[1], hipStream_t stream)
 {
-    p.seg = c.seg;
-    p.enter = enter;
-    p.denter = nullptr;
-    p.by_item = false;
-    p.ticket = nullptr;
+    return launch_linear_walk<T, kOut, kDg>(p[0], stream);
+}
+template <bool kOut, bool kDg, typename T> hipError_t launch(LinearWalk<T> (&p)[2], hipStream_t stream)
+{
+    static_assert(!kDg);
+    return launch_linear_twin<T, kOut>(p[0], p[1], stream);
+}
+
+// The walk, or two that the same states enter, or where rows are cut their steps.
+template <bool kDg, typename T, int N>
+hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* const (&room)[N], hipStream_t stream)
+{
+    for (LinearWalk<T>& w : p) {
+        w.seg = c.seg;
+        w.enter = enter;
+        w.denter = nullptr;
+        w.by_item = false;
+        w.ticket = nullptr;
+    }
+    const DeltaDims& d = p[0].d;
     if (c.seg != kWholeRows && c.chain) {
-        const int64_t columns = linear_columns(sizeof(T), kDg, p.Dv);
-        const int64_t words = p.d.seqs * p.d.nheads * ((p.Dv + columns - 1) / columns) + 1;
-        p.ticket = reinterpret_cast<unsigned*>(states);
-        p.done = p.ticket + 1;
-        p.handed = states + bytes_up(words) / 4;
-        hipLaunchKernelGGL(linear_zero_kernel, dim3(blocks_of(words)), dim3(256), 0, stream, p.ticket, words);
+        int64_t words[2] = {0, 0};
+        for (int i = 0; i < N; ++i) {
+            const int64_t columns = linear_columns(sizeof(T), kDg, p[i].Dv);
+            words[i] = d.seqs * d.nheads * ((p[i].Dv + columns - 1) / columns) + 1;
+            p[i].ticket = reinterpret_cast<unsigned*>(room[i]);
+            p[i].done = p[i].ticket + 1;
+            p[i].handed = room[i] + bytes_up(words[i]) / 4;
+        }
+        hipLaunchKernelGGL(linear_zero_kernel, dim3(blocks_of(words[0] + words[1])), dim3(256), 0, stream, p[0].ticket, words[0],
+                           p[N - 1].ticket, words[1]);
         const hipError_t e = hipGetLastError();
         if (e != hipSuccess) return e;
     } else if (c.seg != kWholeRows) {
-        const int64_t PN = p.d.headdim * p.d.dstate;
-        LinearWalk<T> first = p;
-        first.fin = states;
-        first.dfin = kDg ? states + bytes_up(state_floats(p.d, linear_items(p.d, p.seg))) / 4 : nullptr;
-        hipError_t e = launch_linear_walk<T, false, kDg>(first, stream);
+        const int64_t PN = d.headdim * d.dstate;
+        LinearWalk<T> first[N];
+        for (int i = 0; i < N; ++i) {
+            first[i] = p[i];
+            first[i].fin = room[i];
+            first[i].dfin = kDg ? room[i] + bytes_up(state_floats(d, linear_items(d, c.seg))) / 4 : nullptr;
+            p[i].enter = first[i].fin;
+            p[i].denter = first[i].dfin;
+            p[i].by_item = true;
+        }
+        hipError_t e = launch<false, kDg>(first, stream);
         if (e != hipSuccess) return e;
-        hipLaunchKernelGGL((linear_join_kernel<kDg>), dim3(blocks_of(p.d.seqs * p.d.nheads * PN / 4)), dim3(256), 0, stream,
-                           first.fin, first.dfin, enter, p.g, p.d, p.seg, p.back, PN);
+        hipLaunchKernelGGL((linear_join_kernel<kDg>), dim3(blocks_of(d.seqs * d.nheads * PN / 4), N), dim3(256), 0, stream,
+                           first[0].fin, first[N - 1].fin, first[0].dfin, enter, p[0].g, d, c.seg, p[0].back, PN);
         if ((e = hipGetLastError()) != hipSuccess) return e;
-        p.enter = first.fin;
-        p.denter = first.dfin;
-        p.by_item = true;
     }
-    return launch_linear_walk<T, true, kDg>(p, stream);
+    return launch<true, kDg>(p, stream);
 }
 
 // A workgroup walks one slice of a row and head.  Measured with heads of 64 x 128 over 4096 tokens in bf16, where one row
@@ -161,7 +185,7 @@ hipError_t walk(LinearWalk<T> p, const Cut& c, const float* enter, float* states
 //    that is less than a whole row's chunks take one after another (128 walks: 117 us, whole 139).
 //  - some more than CUs: a few CUs would have one more than the others from the first token to the last. In a chain
 //    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
-//    525, 558; backward of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
+//    525, 558; a backward of three launches of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
 //    the starts are worth.
 //  - rows of different lengths: the same, in pieces of 1024 tokens (20 of up to 1000, 13 heads of 128 x 128: 59 us, cut at
 //    once 102; 7 of 64 to 4096, 80 heads: 230, 346; only 336 walks of 4096 tokens and 256 rows of state are slower, 318, 286).
@@ -199,18 +223,36 @@ Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t leas
 
 // What a chunk takes a walk that runs alone: fp32's matrix products are a sixteenth of bf16's rate, and take it per 32
 // rows of the state.
+double chunk_us(int elem_bytes, bool dg, int64_t Dk) { return (elem_bytes == 2 ? 0.8 + Dk / 512. : 1 + Dk / 34.) * (dg ? 1.6 : 1); }
+int64_t least_chunks(int elem_bytes) { return elem_bytes == 2 ? 8 : 2; }
+int64_t brief_tokens(int elem_bytes) { return elem_bytes == 2 ? 384 : 192; }
+
 Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
     const int columns = linear_columns(elem_bytes, dg, (int)Dv);
-    const double us = (elem_bytes == 2 ? 0.8 + Dk / 512. : 1 + Dk / 34.) * (dg ? 1.6 : 1);
-    return linear_cut(d, (Dv + columns - 1) / columns, us, elem_bytes == 2 ? 8 : 2, elem_bytes == 2 ? 384 : 192);
+    return linear_cut(d, (Dv + columns - 1) / columns, chunk_us(elem_bytes, dg, Dk), least_chunks(elem_bytes), brief_tokens(elem_bytes));
+}
+
+// dk's and dv's walks in one launch, where each has a workgroup for all columns: the GPU is filled as by one walk of twice as
+// many rows, what both read is in the XCD's cache for the second, and where rows are cut there are half the launches. The
+// backward of 320 rows of 64 x 128 over 4096 tokens takes 873 us, with two launches 936; of 192 540, 602; of 160 heads of
+// 128 x 128 807, 949; of 12 rows of 32 x 48 over 501 tokens in fp32 57, 77. None of 22 sizes was slower.
+bool walk_twin(const DeltaDims& d, int elem_bytes, Cut& c)
+{
+    if (d.headdim > 128 || d.dstate > 128) return false;
+    const int cv = linear_columns(elem_bytes, false, (int)d.headdim), ck = linear_columns(elem_bytes, false, (int)d.dstate);
+    const int64_t slices = (d.headdim + cv - 1) / cv + (d.dstate + ck - 1) / ck;
+    c = linear_cut(d, slices, chunk_us(elem_bytes, false, std::max(d.headdim, d.dstate)), least_chunks(elem_bytes),
+                   brief_tokens(elem_bytes));
+    return linear_items(d, c.seg) * d.nheads * slices < (int64_t(1) << 24);
 }
 
 struct GradLayout {
     Cut cq, ck, cv;
+    bool twin;               // dk and dv together
     int64_t items;           // of the walk for dq
     int parts;
-    size_t dpart, dk, dv, total;
+    size_t second, dpart, dk, dv, total;
 };
 
 GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
@@ -219,13 +261,17 @@ GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
     l.cq = walk_cut(d, elem_bytes, true, d.headdim, d.dstate);
     l.ck = walk_cut(d, elem_bytes, false, d.headdim, d.dstate);
     l.cv = walk_cut(d, elem_bytes, false, d.dstate, d.headdim);
+    Cut both;
+    l.twin = walk_twin(d, elem_bytes, both);
+    if (l.twin) l.ck = l.cv = both;
     l.items = linear_items(d, l.cq.seg);
     const int columns = linear_columns(elem_bytes, true, (int)d.dstate);
     l.parts = (int)((d.dstate + columns - 1) / columns) * linear_waves(elem_bytes, true, (int)d.dstate);
-    // (the walks run one after another: one room for their states)
-    l.dpart = std::max({walk_bytes(d, l.cq, elem_bytes, true, d.headdim, d.dstate),
-                        walk_bytes(d, l.ck, elem_bytes, false, d.headdim, d.dstate),
-                        walk_bytes(d, l.cv, elem_bytes, false, d.dstate, d.headdim)});
+    // (walks that run one after another share a room for their states)
+    const size_t bk = walk_bytes(d, l.ck, elem_bytes, false, d.headdim, d.dstate),
+                 bv = walk_bytes(d, l.cv, elem_bytes, false, d.dstate, d.headdim);
+    l.second = l.twin ? bk : 0;
+    l.dpart = std::max({walk_bytes(d, l.cq, elem_bytes, true, d.headdim, d.dstate), bk, l.second + bv});
     l.dk = l.dpart + bytes_up(l.items * d.nheads * l.parts);
     const bool shared = d.nheads != d.ngroups;
     l.dv = l.dk + (shared ? bytes_up(d.tokens * d.nheads * d.dstate) : 0);
@@ -259,7 +305,8 @@ hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T
                                  float* fin, const DeltaDims& d, void* workspace, hipStream_t stream)
 {
     const int share = (int)(d.nheads / d.ngroups);
-    LinearWalk<T> p{};
+    LinearWalk<T> w[1]{};
+    LinearWalk<T>& p = w[0];
     p.q = {q, d.nheads * d.dstate, 1};
     p.k = {k, d.ngroups * d.dstate, share};
     p.v = {v, d.ngroups * d.headdim, share};
@@ -271,7 +318,7 @@ hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T
     p.Dk = (int)d.dstate;
     p.Dv = (int)d.headdim;
     p.d = d;
-    return walk<T, false>(p, walk_cut(d, sizeof(T), false, d.dstate, d.headdim), init, static_cast<float*>(workspace), stream);
+    return walk<false>(w, walk_cut(d, sizeof(T), false, d.dstate, d.headdim), init, {static_cast<float*>(workspace)}, stream);
 }
 
 template <typename T>
@@ -287,7 +334,8 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     const bool shared = share > 1;
     const LinearOperand<T> oq = {q, d.nheads * d.dstate, 1}, ok = {k, d.ngroups * d.dstate, share},
                            ov = {v, d.ngroups * d.headdim, share}, od = {dy, d.nheads * d.headdim, 1};
-    LinearWalk<T> p{};
+    LinearWalk<T> wq[1]{};
+    LinearWalk<T>& p = wq[0];
     p.g = g;
     p.d = d;
     // dq: the rows of the walk's state are the state's rows, its columns the columns
@@ -302,33 +350,45 @@ hipError_t launch_linear_backward(const T* v, const float* g, const T* k, const 
     p.Dv = (int)d.dstate;
     p.dlast = dfinal;
     p.dpart = dpart;
-    hipError_t e = walk<T, true>(p, l.cq, init, states, stream);
+    hipError_t e = walk<true>(wq, l.cq, init, {states}, stream);
     if (e != hipSuccess) return e;
     hipLaunchKernelGGL(linear_dg_kernel, dim3((unsigned)d.nheads), dim3(256), 0, stream, dpart, dg, l.items, d.nheads,
                        l.parts);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     // dk
-    p.q = ov;
-    p.k = od;
-    p.v = oq;
-    p.x = {};
-    p.dlast = nullptr;
-    p.dpart = nullptr;
-    p.back = true;
-    p.of32 = shared;
-    p.o = shared ? static_cast<void*>(ws + l.dk) : dk;
-    if ((e = walk<T, false>(p, l.ck, dfinal, states, stream)) != hipSuccess) return e;
+    LinearWalk<T> wk{};
+    wk.g = g;
+    wk.d = d;
+    wk.q = ov;
+    wk.k = od;
+    wk.v = oq;
+    wk.back = true;
+    wk.of32 = shared;
+    wk.o = shared ? static_cast<void*>(ws + l.dk) : dk;
+    wk.sk = d.dstate;
+    wk.sv = 1;
+    wk.Dk = (int)d.headdim;
+    wk.Dv = (int)d.dstate;
     // dv, and the gradient of the state before the first token
-    p.q = ok;
-    p.k = oq;
-    p.v = od;
-    p.o = shared ? static_cast<void*>(ws + l.dv) : dv;
-    p.sk = 1;
-    p.sv = d.dstate;
-    p.Dk = (int)d.dstate;
-    p.Dv = (int)d.headdim;
-    p.fin = dinit;
-    if ((e = walk<T, false>(p, l.cv, dfinal, states, stream)) != hipSuccess) return e;
+    LinearWalk<T> wv = wk;
+    wv.q = ok;
+    wv.k = oq;
+    wv.v = od;
+    wv.o = shared ? static_cast<void*>(ws + l.dv) : dv;
+    wv.sk = 1;
+    wv.sv = d.dstate;
+    wv.Dk = (int)d.dstate;
+    wv.Dv = (int)d.headdim;
+    wv.fin = dinit;
+    if (l.twin) {
+        LinearWalk<T> w[2] = {wk, wv};
+        if ((e = walk<false>(w, l.ck, dfinal, {states, states + l.second / 4}, stream)) != hipSuccess) return e;
+    } else {
+        LinearWalk<T> w[1] = {wk};
+        if ((e = walk<false>(w, l.ck, dfinal, {states}, stream)) != hipSuccess) return e;
+        w[0] = wv;
+        if ((e = walk<false>(w, l.cv, dfinal, {states}, stream)) != hipSuccess) return e;
+    }
     if (shared && d.tokens > 0) {
         const int64_t rows = d.tokens * d.ngroups;
         hipLaunchKernelGGL((linear_group_kernel<T>), dim3(blocks_of(rows * d.dstate / 4)), dim3(256), 0, stream,

@@ -9,10 +9,12 @@
 
 namespace ssd {
 
+template <typename T> constexpr int kWalkLds = (sizeof(T) == 2 ? 80 : 160) * 1024;
+
 template <typename T, int NW, int JT, bool kOut, bool kDg>
 hipError_t walk_kb(const LinearWalk<T>& p, hipStream_t stream)
 {
-#define SSD_WALK(KB) return launch_walk<T, KB, NW, JT, (sizeof(T) == 2 ? 80 : 160) * 1024, kOut, kDg>(p, stream)
+#define SSD_WALK(KB) return launch_walk<T, KB, NW, JT, kWalkLds<T>, kOut, kDg>(p, stream)
     if (p.Dk <= 32) SSD_WALK(1);
     if (p.Dk <= 64) SSD_WALK(2);
     if (p.Dk <= 128) SSD_WALK(4);
@@ -32,6 +34,21 @@ hipError_t launch_linear_walk(const LinearWalk<T>& p, hipStream_t stream)
             if (linear_columns(sizeof(T), false, p.Dv) == 128) return walk_kb<T, 4, 2, kOut, kDg>(p, stream);
         return walk_kb<T, 4, 1, kOut, kDg>(p, stream);
     }
+}
+
+template <typename T, bool kOut>
+hipError_t launch_linear_twin(const LinearWalk<T>& a, const LinearWalk<T>& b, hipStream_t stream)
+{
+#define SSD_TWIN(KB)                                                                                                   \
+    do {                                                                                                               \
+        if (b.Dk <= 32) return launch_twin<T, KB, 1, kWalkLds<T>, kOut>(a, b, stream);                                 \
+        if (b.Dk <= 64) return launch_twin<T, KB, 2, kWalkLds<T>, kOut>(a, b, stream);                                 \
+        return launch_twin<T, KB, 4, kWalkLds<T>, kOut>(a, b, stream);                                                 \
+    } while (0)
+    if (a.Dk <= 32) SSD_TWIN(1);
+    if (a.Dk <= 64) SSD_TWIN(2);
+    SSD_TWIN(4);
+#undef SSD_TWIN
 }
 
 }  // namespace ssd

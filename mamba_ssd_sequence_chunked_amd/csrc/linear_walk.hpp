@@ -401,10 +401,9 @@ __device__ __forceinline__ void lds_half(Vec8<float>& f, unsigned a)
     for (int m = 0; m < 4; ++m) { f.v[m] = x[m]; f.v[4 + m] = 0.f; }
 }
 
+// Workgroup `block` of the `blocks` of a walk.
 template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
-__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(
-    LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves, LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves)))
-void linear_walk_kernel(LinearWalk<T> p)
+__device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int block, int blocks)
 {
     using S = LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>;
     constexpr int CHk = S::CHk, CHv = S::CHv, kNT = 2 * KB, kStages = S::kStages;
@@ -441,11 +440,11 @@ void linear_walk_kernel(LinearWalk<T> p)
             const unsigned walks = (unsigned)p.d.seqs * of_row;
             turn = __builtin_amdgcn_readfirstlane(mine / walks);
             walk = __builtin_amdgcn_readfirstlane(xcd_logical_block((int)(mine - turn * walks), (int)walks));
-            const unsigned per = __builtin_amdgcn_readfirstlane(gridDim.x / walks), row = walk / of_row;
+            const unsigned per = __builtin_amdgcn_readfirstlane((unsigned)blocks / walks), row = walk / of_row;
             at = (row * per + (p.back ? per - 1 - turn : turn)) * of_row + (walk - row * of_row);
         }
     } else {
-        at = xcd_logical_block(blockIdx.x, gridDim.x);
+        at = xcd_logical_block(block, blocks);
     }
     at = __builtin_amdgcn_readfirstlane(at);                      // (fewer than 2^24 workgroups)
     const int slice = at % slices, h = at / slices % H;
@@ -917,19 +916,73 @@ void linear_walk_kernel(LinearWalk<T> p)
     }
 }
 
+template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
+__global__ __launch_bounds__(NW * 64) __attribute__((amdgpu_waves_per_eu(
+    LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves, LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>::kWaves)))
+void linear_walk_kernel(LinearWalk<T> p)
+{
+    linear_walk_run<T, KB, NW, JT, kBudget, kOut, kDg>(p, blockIdx.x, gridDim.x);
+}
+
+// Two walks in one launch: dk's and dv's, whose rows and columns of the state are each other's.
+template <typename T, int KB, int KB2, int kBudget, bool kOut> struct LinearTwin {
+    static constexpr int JT = sizeof(T) == 2 && KB2 > 2 ? 2 : 1, JT2 = sizeof(T) == 2 && KB > 2 ? 2 : 1;
+    using A = LinearShape<T, KB, 4, JT, kBudget, kOut, false>;
+    using B = LinearShape<T, KB2, 4, JT2, kBudget, kOut, false>;
+    static constexpr int kWaves = A::kWaves < B::kWaves ? A::kWaves : B::kWaves;
+    static constexpr int kLds = A::kLds > B::kLds ? A::kLds : B::kLds;
+};
+template <typename T, int KB, int KB2, int kBudget, bool kOut>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(LinearTwin<T, KB, KB2, kBudget, kOut>::kWaves,
+                                                                     LinearTwin<T, KB, KB2, kBudget, kOut>::kWaves)))
+void linear_twin_kernel(LinearWalk<T> a, LinearWalk<T> b, int blocks_a)
+{
+    using W = LinearTwin<T, KB, KB2, kBudget, kOut>;
+    // eight of one (a workgroup for each XCD), eight of the other: segments that wait in a chain start behind both's first ones
+    const int blocks_b = gridDim.x - blocks_a, pairs = min(blocks_a, blocks_b) & ~7, block = blockIdx.x;
+    bool second;
+    int at;
+    if (block < 2 * pairs) {
+        second = block >> 3 & 1;
+        at = (block >> 4) * 8 + (block & 7);
+    } else {
+        at = block - pairs;
+        second = at >= blocks_a;
+        if (second) at -= blocks_a - pairs;
+    }
+    if (!second) linear_walk_run<T, KB, 4, W::JT, kBudget, kOut, false>(a, at, blocks_a);
+    else linear_walk_run<T, KB2, 4, W::JT2, kBudget, kOut, false>(b, at, blocks_b);
+}
+
 // ---- launches -------------------------------------------------------------------------------------------
+
+template <typename T> int64_t walk_blocks(const LinearWalk<T>& p, int columns)
+{
+    return linear_items(p.d, p.seg) * p.d.nheads * ((p.Dv + columns - 1) / columns);
+}
 
 template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
 hipError_t launch_walk(const LinearWalk<T>& p, hipStream_t stream)
 {
     using S = LinearShape<T, KB, NW, JT, kBudget, kOut, kDg>;
     static_assert(S::kLds <= 160 * 1024, "the ring fits LDS");
-    const int64_t slices = (p.Dv + NW * JT * 16 - 1) / (NW * JT * 16);
-    const int64_t blocks = linear_items(p.d, p.seg) * p.d.nheads * slices;
+    const int64_t blocks = walk_blocks(p, NW * JT * 16);
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((linear_walk_kernel<T, KB, NW, JT, kBudget, kOut, kDg>), dim3((unsigned)blocks), dim3(NW * 64),
                        // (a chain's segments one to a CU: one that waits takes no other's turn)
                        p.ticket ? std::max(S::kLds, 84 * 1024) : S::kLds, stream, p);
+    return hipGetLastError();
+}
+
+template <typename T, int KB, int KB2, int kBudget, bool kOut>
+hipError_t launch_twin(const LinearWalk<T>& a, const LinearWalk<T>& b, hipStream_t stream)
+{
+    using W = LinearTwin<T, KB, KB2, kBudget, kOut>;
+    static_assert(W::kLds <= 160 * 1024, "the rings fit LDS");
+    const int64_t first = walk_blocks(a, 64 * W::JT), blocks = first + walk_blocks(b, 64 * W::JT2);
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL((linear_twin_kernel<T, KB, KB2, kBudget, kOut>), dim3((unsigned)blocks), dim3(256),
+                       a.ticket ? std::max(W::kLds, 84 * 1024) : W::kLds, stream, a, b, (int)first);
     return hipGetLastError();
 }
 
@@ -946,5 +999,9 @@ constexpr int64_t linear_handed(int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 
 template <typename T, bool kOut, bool kDg>
 hipError_t launch_linear_walk(const LinearWalk<T>& p, hipStream_t stream);
+
+// Two walks, a's rows and columns b's columns and rows, at most 128 of each.
+template <typename T, bool kOut>
+hipError_t launch_linear_twin(const LinearWalk<T>& a, const LinearWalk<T>& b, hipStream_t stream);
 
 }  // namespace ssd

@@ -7,7 +7,7 @@ import pytest
 import linear_ref as ref
 from test_gpu_delta_guard import call, typed
 from test_gpu_guard import Guarded, _code, _lib, _p, _stream
-from test_gpu_linear import check, dev, f64, inputs
+from test_gpu_linear import ROUND, check, dev, dg_unit, hold, inputs, state_unit, y_unit
 
 pytestmark = pytest.mark.gpu
 
@@ -294,3 +294,25 @@ def test_captured_packed_with_other_offsets(H, T):
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("b,L,H,G,dt", [(1, 40, 9, 3, "bf16"), (1, 2100, 3, 3, "bf16"), (1, 300, 5, 1, "f32"), (2, 2048, 75, 75, "bf16")])
+@pytest.mark.parametrize("P,N", [(16, 32), (32, 48), (64, 16), (48, 112), (128, 64), (112, 128), (16, 144)])
+def test_backward_of_each_width(b, L, H, G, P, N, dt):
+    """Every pairing of the widths that the backward's walks are made for: whole rows, rows cut at once and chains.  The
+    last group's heads against the formulas, and the call again."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(b, L, H, P, N, G, dt, True, seed=820)
+    (v, g, k, q), h, dy, df = inputs(d), dev(d["init"]), dev(d["dy"], dt), dev(d["dfinal"])
+    got = ssd.linear_backward(v, g, k, q, dy, h, df)
+    again = ssd.linear_backward(v, g, k, q, dy, h, df)
+    assert all(torch.equal(got[n], again[n]) for n in got)
+    m = H // G
+    want, size = ref.backward(d["v"][:, :, -1:], d["g"][-m:], d["k"][:, :, -1:], d["q"][:, :, -m:], d["dy"][:, :, -m:],
+                              d["init"][:, -m:], d["dfinal"][:, -m:])
+    hold("dv", got["dv"][:, :, -1:], want["dv"], size["dv"], y_unit(dt, L, N, P))
+    hold("dk", got["dk"][:, :, -1:], want["dk"], size["dk"], y_unit(dt, L, N, P))
+    hold("dq", got["dq"][:, :, -m:], want["dq"], size["dq"], y_unit(dt, L, N, P))
+    hold("dinit", got["dinit"][:, -m:], want["dinit"], size["dinit"], state_unit(dt, L, N, P))
+    hold("dg", got["dg"][-m:], want["dg"], size["dg"], dg_unit(dt, L, N, P) + b * ROUND["f32"])
