@@ -396,21 +396,22 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  * q is a head's own; head h reads k and v of group h / (nheads / ngroups), ngroups = nheads where nothing is shared.
  * Conventions and errors are those at the top of this header, and:
  *   - g float (nheads) is the log decay, <= 0 and constant in time; it is not clamped, except that every g below
- *     -1000 acts as -1000, so -inf leaves each token alone. A power of the decay below 2^-126 (exp(-87)) is 0. g = 0 is plain causal
- *     linear attention. No scale is applied to q.
+ *     -1000 acts as -1000, so -inf leaves each token alone. A power of the decay below 2^-126 (exp(-87)) is 0. g = 0
+ *     is plain causal linear attention. No scale is applied to q.
  *   - headdim and dstate are multiples of 16 in [16, 256]; nheads * headdim and nheads * dstate <= 2^20; 0 <= batch <=
  *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
  *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate
  *     < 2^34, tokens * ngroups * the wider < 2^34; for ssd_linear_step batch * nheads * headdim < 2^28.
  *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (5e-7 of their norm, dg 4e-6 where its terms
- *     cancel): what leads to them is carried as two or three bf16 values. bf16 outputs are a little further off than their own rounding (1.7e-3 of the
- *     norm), because the scores and, where they are read, the states are rounded to bf16 on the way: up to 2.6e-3.
- *     With fp32 inputs everything is fp32.
+ *     cancel): what leads to them is carried as two or three bf16 values. bf16 outputs are a little further off than
+ *     their own rounding (1.7e-3 of the norm), because the scores and, where they are read, the states are rounded to
+ *     bf16 on the way: up to 2.6e-3. With fp32 inputs everything is fp32.
  *   - Sums are made in a fixed order: the same call gives the same bits.
- *   - Non-finite inputs: tokens are summed in chunks of up to 64 (of their sequence or of a segment of it) in which later tokens
- *     have a weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of its chunk (and all
- *     later ones), of the heads that read it, never another sequence, batch row or group. A gradient's chunks go from the
- *     end: there it can reach later tokens of the chunk and all earlier ones.
+ *   - Non-finite inputs: tokens are summed in chunks of 32 (of their sequence or of a segment of it) in which later
+ *     tokens have a weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of its chunk and
+ *     all later ones (where the decay has left nothing of it, it need not), of the heads that read it, never another
+ *     sequence, batch row or group. dk's and dv's chunks go from the end: there it can reach later tokens of the
+ *     chunk and all earlier ones.
  * ------------------------------------------------------------------------------------------- */
 
 /* y, final_states over whole sequences.

@@ -2,7 +2,8 @@
 //
 //   S[p, n] = a S[p, n] + v[p] k[n];   y[p] = sum_n S[p, n] q[n],   a = exp(g)
 //
-// The fp32 state is read and written once, 5 flops an element: bound by HBM bandwidth.  A thread owns 4
+// The fp32 state is read and written once, 5 flops an element: bound by HBM bandwidth (240 of 256 rows, 80 heads of 64 x 128:
+// 227 to 233 us, 5.5 TB/s; 13 rows, 20 heads of 128 x 256 13.7 us, 5.0 TB/s).  One row of 24 heads is the launch, 6 us.  A thread owns 4
 // consecutive columns of every (256 / W)-th row, W lanes to a row (a power of two >= N / 4; surplus lanes contribute 0),
 // and kPass rows; a workgroup has kPass * 256 / W rows of one (batch row, head).  All its rows are on the way before any
 // arithmetic, non-temporal, as in ssd_step.  Large heads take several workgroups: with one each a CU's reads and
