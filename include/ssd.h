@@ -397,7 +397,7 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  * Conventions and errors are those at the top of this header, and:
  *   - g float (nheads) is the log decay, <= 0 and constant in time; it is not clamped, except that every g below
  *     -1000 acts as -1000, so -inf leaves each token alone. A power of the decay below 2^-126 (exp(-87)) is 0. g = 0
- *     is plain causal linear attention. No scale is applied to q.
+ *     is plain causal linear attention. A NaN makes all of its head's results NaN. No scale is applied to q.
  *   - headdim and dstate are multiples of 16 in [16, 256]; nheads * headdim and nheads * dstate <= 2^20; 0 <= batch <=
  *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
  *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate

@@ -193,6 +193,9 @@ size_t delta_backward_workspace(const DeltaDims& d, int elem_bytes);
 
 // ---- linear attention with a decay for each head (the "linear" entry points) and pools of states ------
 
+// The log decay as it acts: -1000 below that (so that powers of it stay numbers); NaN stays.
+__device__ __forceinline__ float linear_rate(float g) { return g < -1000.f ? -1000.f : g; }
+
 // (DeltaDims, with k and v shared by the heads of a group and q a head's own)
 template <typename T>
 hipError_t launch_linear_forward(const T* v, const float* g, const T* k, const T* q, const float* init, T* y,

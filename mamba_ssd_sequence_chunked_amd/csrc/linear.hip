@@ -38,7 +38,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ lo
         n = d.seqlen;
     }
     const int64_t count = max((n + seg - 1) / seg, (int64_t)1);
-    const float gl = fmaxf(g[h], -1000.f);
+    const float gl = linear_rate(g[h]);
     LinearDecay decay;
     decay.set(gl, (int)min(seg, n));
     f32x4 s = {0.f, 0.f, 0.f, 0.f}, ds = {0.f, 0.f, 0.f, 0.f};

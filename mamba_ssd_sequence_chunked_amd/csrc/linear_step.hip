@@ -48,7 +48,7 @@ __global__ __launch_bounds__(256) void linear_step_kernel(
         s[i] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (ok && live && colok) s[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(S + (int64_t)p * N + col));
     }
-    const float a = expf(fmaxf(gv[h], -1000.f));
+    const float a = expf(linear_rate(gv[h]));
     float kv[4] = {0.f, 0.f, 0.f, 0.f}, qv[4] = {0.f, 0.f, 0.f, 0.f};
     if (colok) {
         const float4 k4 = load4f(Km + grp * N + col), q4 = load4f(Qm + (int64_t)bh * N + col);

@@ -461,7 +461,7 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
     // where the walk's own columns of the state lie
     const int col0 = slice * NW * JT * 16;
     const int validk = p.Dk * S::kEs / 16, validv = min(CHv, (p.Dv - col0) * S::kEs / 16);
-    const float gl = fmaxf(p.g[h], -1000.f);
+    const float gl = linear_rate(p.g[h]);
     if constexpr (!kOut) {
         // What a token adds to the state n tokens later is 0 in fp32 where a^n is below e^-200, whatever finite values it
         // has (their product is below e^89, and 0 begins at e^-103): the walk starts where something is left.

@@ -316,3 +316,27 @@ def test_backward_of_each_width(b, L, H, G, P, N, dt):
     hold("dq", got["dq"][:, :, -m:], want["dq"], size["dq"], y_unit(dt, L, N, P))
     hold("dinit", got["dinit"][:, -m:], want["dinit"], size["dinit"], state_unit(dt, L, N, P))
     hold("dg", got["dg"][-m:], want["dg"], size["dg"], dg_unit(dt, L, N, P) + b * ROUND["f32"])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("L", [40, 3000])
+def test_nan_decay_shows_in_its_head(L, dt):
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    H, P, N, G = 4, 32, 48, 2
+    v, g, k, q = inputs(ref.make(1, L, H, P, N, G, dt, False, seed=830))
+    bad = g.clone()
+    bad[1] = float("nan")                                    # of heads 0 and 1, which share a key
+    rest = torch.tensor([0, 2, 3], device="cuda")
+    (y, fin), (yr, fr) = ssd.linear_forward(v, bad, k, q), ssd.linear_forward(v, g, k, q)
+    assert y[:, :, 1].isnan().all() and fin[:, 1].isnan().all()
+    assert torch.equal(y[:, :, rest], yr[:, :, rest]) and torch.equal(fin[:, rest], fr[:, rest])
+    b, br = ssd.linear_backward(v, bad, k, q, yr), ssd.linear_backward(v, g, k, q, yr)
+    assert b["dg"][1].isnan() and b["dinit"][:, 1].isnan().all() and b["dq"][:, :, 1].isnan().all()
+    assert b["dk"][:, :, 0].isnan().all() and b["dv"][:, :, 0].isnan().all()
+    assert all(torch.equal(b[n][:, :, 1], br[n][:, :, 1]) for n in ("dk", "dv")) and torch.equal(b["dg"][rest], br["dg"][rest])
+    one = [t[:, 0].contiguous() for t in (v, k, q)]
+    s, sr = torch.ones((1, H, P, N), device="cuda"), torch.ones((1, H, P, N), device="cuda")
+    y, yr = ssd.linear_step(s, one[0], bad, one[1], one[2]), ssd.linear_step(sr, one[0], g, one[1], one[2])
+    assert y[:, 1].isnan().all() and s[:, 1].isnan().all()
+    assert torch.equal(y[:, rest], yr[:, rest]) and torch.equal(s[:, rest], sr[:, rest])
