@@ -340,3 +340,56 @@ def test_nan_decay_shows_in_its_head(L, dt):
     y, yr = ssd.linear_step(s, one[0], bad, one[1], one[2]), ssd.linear_step(sr, one[0], g, one[1], one[2])
     assert y[:, 1].isnan().all() and s[:, 1].isnan().all()
     assert torch.equal(y[:, rest], yr[:, rest]) and torch.equal(s[:, rest], sr[:, rest])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_widest_rows(dt):
+    """A token's row of 2^20 elements, the most that is taken: each head as by itself."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    H, P, N, L, T = 4096, 256, 256, 37, typed(dt)
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda", dtype=T)          # noqa: E731
+    v, k, q, dy = rand(1, L, H // 2, P), rand(1, L, H // 2, N), rand(1, L, H, N), rand(1, L, H, P)
+    g = -torch.rand(H, generator=gen, device="cuda")
+    y, fin = ssd.linear_forward(v, g, k, q)
+    for h in (0, 4095, 2047):
+        pick = lambda t, i: t[:, :, i:i + 1].contiguous()                            # noqa: E731
+        a, b = ssd.linear_forward(pick(v, h // 2), g[h:h + 1].contiguous(), pick(k, h // 2), pick(q, h))
+        assert torch.equal(y[:, :, h:h + 1], a) and torch.equal(fin[:, h:h + 1], b)
+    del y, fin
+    got = ssd.linear_backward(v, g, k, q, dy)
+    for h in (0, 4094):
+        pair = lambda t: t[:, :, h:h + 2].contiguous()                               # noqa: E731
+        one = ssd.linear_backward(pick(v, h // 2), g[h:h + 2].contiguous(), pick(k, h // 2), pair(q), pair(dy))
+        assert torch.equal(got["dq"][:, :, h:h + 2], one["dq"]) and torch.equal(got["dinit"][:, h:h + 2], one["dinit"])
+        assert torch.equal(got["dk"][:, :, h // 2:h // 2 + 1], one["dk"]) and torch.equal(got["dv"][:, :, h // 2:h // 2 + 1], one["dv"])
+        assert torch.equal(got["dg"][h:h + 2], one["dg"])
+    with pytest.raises(ssd.SSDError):                        # 2^20 + 256
+        ssd.linear_forward(*(torch.empty(s, dtype=T, device="cuda") if len(s) > 1 else torch.zeros(s, device="cuda")
+                             for s in ((1, 1, 1, P), (H + 1,), (1, 1, 1, N), (1, 1, H + 1, N))))
+
+
+def test_most_rows_of_one_token():
+    """65535 rows of a token, each from its state: what a step does, forwards and back."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    b, H, P, N = 65535, 2, 16, 16
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    rand = lambda *s: torch.randn(s, generator=gen, device="cuda")                   # noqa: E731
+    v, k, q, h, dy, g = rand(b, 1, 1, P), rand(b, 1, 1, N), rand(b, 1, H, N), rand(b, H, P, N), rand(b, 1, H, P), -rand(H).abs()
+    y, fin = ssd.linear_forward(v, g, k, q, h)
+    state = h.clone()
+    ys = ssd.linear_step(state, v[:, 0], g, k[:, 0], q[:, 0])
+    # the same few fp32 sums in another order: 16 terms of a token's output, each rounded twice, 2 of a state's element
+    assert (y[:, 0] - ys).norm() <= 2.0 ** -24 * 33 ** 0.5 * 2 * ys.norm() and (fin - state).norm() <= 2.0 ** -22 * state.norm()
+    got = ssd.linear_backward(v, g, k, q, dy, h)
+    D = dy[:, 0, :, :, None].double() * q[:, 0, :, None, :].double()
+    a = g.double().exp()[:, None, None]
+    want = dict(dinit=a * D, dv=(D * k[:, 0, :, None, :]).sum((1, 3))[:, None, None], dk=(D * v[:, 0, :, :, None]).sum((1, 2))[:, None, None],
+                dq=(dy[:, 0, :, :, None].double() * state).sum(2)[:, None], dg=(D * a * h).sum((0, 2, 3)))
+    for n, w in want.items():
+        # dg: a row's 256 terms, rounded 3 times each and added in fp32 in chains of 16 and a tree of 64 lanes: fewer than 64
+        # roundings of at most the terms' 2-norm, their signs being random, doubled; rows are added in 64 bits
+        size, count = ((D * a * h).square().sum((0, 2, 3)).sqrt().norm(), 64) if n == "dg" else (w.norm(), 33)
+        assert (got[n].double() - w).norm() <= 2.0 ** -24 * count ** 0.5 * 2 * size, n
