@@ -402,8 +402,8 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
  *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate
  *     < 2^34, tokens * ngroups * the wider < 2^34; for ssd_linear_step batch * nheads * headdim < 2^28.
- *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (5e-7 of their norm, dg 4e-6 where its terms
- *     cancel): what leads to them is carried as two or three bf16 values. bf16 outputs are a little further off than
+ *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (5e-7 of their norm, dg 2e-6 where its terms
+ *     cancel): what leads to them is carried as three bf16 values. bf16 outputs are a little further off than
  *     their own rounding (1.7e-3 of the norm), because the scores and, where they are read, the states are rounded to
  *     bf16 on the way: up to 2.6e-3. With fp32 inputs everything is fp32.
  *   - Sums are made in a fixed order: the same call gives the same bits.

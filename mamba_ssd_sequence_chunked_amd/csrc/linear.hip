@@ -116,7 +116,7 @@ int64_t state_floats(const DeltaDims& d, int64_t items) { return items * d.nhead
 // How the rows of a walk are run: whole, cut into segments that walk at once (with a pass before), or in a chain.
 struct Cut {
     int64_t seg;
-    bool chain;
+    bool chain, alone;       // alone: the chain's workgroups have a CU each
 };
 
 __global__ __launch_bounds__(256) void linear_zero_kernel(unsigned* p, int64_t n, unsigned* p2, int64_t n2)
@@ -165,6 +165,7 @@ hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* 
             p[i].ticket = reinterpret_cast<unsigned*>(room[i]);
             p[i].done = p[i].ticket + 1;
             p[i].handed = room[i] + bytes_up(words[i]) / 4;
+            p[i].alone = c.alone;
         }
         hipLaunchKernelGGL(linear_zero_kernel, dim3(blocks_of(words[0] + words[1])), dim3(256), 0, stream, p[0].ticket, words[0],
                            p[N - 1].ticket, words[1]);
@@ -196,8 +197,12 @@ hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* 
 //    that is less than a whole row's chunks take one after another (128 walks: 117 us, whole 139).
 //  - some more than CUs: a few CUs would have one more than the others from the first token to the last. In a chain
 //    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
-//    525, 558; a backward of three launches of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for fewer tokens than
-//    the starts are worth.
+//    525, 558; a backward of three launches of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for
+//    fewer tokens than the starts are worth. Two workgroups share a CU from 512 walks on (heads of 64 x 256, 640 walks: 575, alone
+//    683; the backward's two launches together 843, 854); fewer rows do not keep two busy, since segments behind their row's
+//    first one wait (the backward of 160 heads of 128 x 128: 787, not alone 843). As many segments as leave the fewest
+//    CUs idle at the end (288 walks: 2 take 243, 3 229, 4 229; 352: 256, 287, 277; 576: 430, 414, 412). Towards dg, where two on a
+//    CU take as long as one after the other, a CU counts once (the backward of 640: 2 take 1594, 4 1645), and in fp32.
 //  - rows of different lengths: the same, in pieces of 1024 tokens (20 of up to 1000, 13 heads of 128 x 128: 59 us, cut at
 //    once 102; 7 of 64 to 4096, 80 heads: 230, 346; only 336 walks of 4096 tokens and 256 rows of state are slower, 318, 286).
 //    Whole where they are short, 384 tokens on average: a chain's workgroups have a CU each, and so little to walk is
@@ -206,14 +211,15 @@ hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* 
 //    300 166, 147). With many walks all CUs are busy in any case (2048: 141, whole 128).
 //    Few walks are cut at once, since one long row would walk alone, but into three at least, as above.
 constexpr double kStartsUs = 9;      // what two launches more take
-Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t least_chunks, int64_t brief)
+constexpr double kStartChunks = 3;   // a segment's start in a chain, in chunks
+Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t least_chunks, int64_t brief, bool one)
 {
     constexpr int64_t kCUs = 256, kLeast = 256;
     const int64_t walks = d.seqs * d.nheads * slices, over = walks % (2 * kCUs);
-    Cut c{kWholeRows, false};
+    Cut c{kWholeRows, false, false};
     if (d.cu) {
         if (walks >= 4 * kCUs || (d.tokens <= brief * d.seqs && walks > kCUs)) return c;
-        c.chain = walks > kCUs && d.seqs <= kChainRows;
+        c.chain = c.alone = walks > kCUs && d.seqs <= kChainRows;
         c.seg = c.chain ? 1024 : std::max<int64_t>(2 * kLeast, d.tokens * d.nheads * slices / (4 * kCUs));
     } else if (walks < kCUs) {
         const int64_t chunks = (d.seqlen + kLC - 1) / kLC;
@@ -221,14 +227,21 @@ Cut linear_cut(const DeltaDims& d, int64_t slices, double chunk_us, int64_t leas
         if (n <= 2 || chunks * chunk_us * (n - 2) / n < kStartsUs) return c;
         c.seg = (d.seqlen + n - 1) / n;
     } else if (walks > kCUs && walks < 4 * kCUs && over > 0 && over <= 3 * kCUs / 2 && d.seqlen >= 8 * kLeast) {
-        const int64_t n = walks < 11 * kCUs / 8 ? 3 : 2;
-        c.seg = (d.seqlen + n - 1) / n;
         c.chain = true;
+        c.alone = walks < 2 * kCUs;
+        const int64_t slots = c.alone || one ? kCUs : 2 * kCUs;
+        int64_t n = 2;
+        double least = 0;
+        for (int64_t i = 2; i <= 4; ++i) {
+            const double took = (double)((walks * i + slots - 1) / slots) * (1. / i + kStartChunks * kLC / d.seqlen);
+            if (i == 2 || took < least) { least = took; n = i; }
+        }
+        c.seg = (d.seqlen + n - 1) / n;
     } else {
         return c;
     }
     c.seg = (c.seg + 63) / 64 * 64;
-    if (d.cu ? d.tokens <= (c.chain ? 1 : 2) * c.seg : d.seqlen <= c.seg) return Cut{kWholeRows, false};
+    if (d.cu ? d.tokens <= (c.chain ? 1 : 2) * c.seg : d.seqlen <= c.seg) return Cut{kWholeRows, false, false};
     return c;
 }
 
@@ -241,7 +254,8 @@ int64_t brief_tokens(int elem_bytes) { return elem_bytes == 2 ? 384 : 192; }
 Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
     const int columns = linear_columns(elem_bytes, dg, (int)Dv);
-    return linear_cut(d, (Dv + columns - 1) / columns, chunk_us(elem_bytes, dg, Dk), least_chunks(elem_bytes), brief_tokens(elem_bytes));
+    return linear_cut(d, (Dv + columns - 1) / columns, chunk_us(elem_bytes, dg, Dk), least_chunks(elem_bytes),
+                      brief_tokens(elem_bytes), dg || elem_bytes == 4);
 }
 
 // dk's and dv's walks in one launch, where each has a workgroup for all columns: the GPU is filled as by one walk of twice as
@@ -254,7 +268,7 @@ bool walk_twin(const DeltaDims& d, int elem_bytes, Cut& c)
     const int cv = linear_columns(elem_bytes, false, (int)d.headdim), ck = linear_columns(elem_bytes, false, (int)d.dstate);
     const int64_t slices = (d.headdim + cv - 1) / cv + (d.dstate + ck - 1) / ck;
     c = linear_cut(d, slices, chunk_us(elem_bytes, false, std::max(d.headdim, d.dstate)), least_chunks(elem_bytes),
-                   brief_tokens(elem_bytes));
+                   brief_tokens(elem_bytes), elem_bytes == 4);
     return linear_items(d, c.seg) * d.nheads * slices < (int64_t(1) << 24);
 }
 

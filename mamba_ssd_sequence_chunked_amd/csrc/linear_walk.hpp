@@ -33,8 +33,8 @@
 // into a chain: one launch in which a segment takes over the state when the one before it is done.
 //
 // What bounds it, and what it takes (bf16, heads of 64 x 128, 4096 tokens): 320 rows 246 us, 4.1 TB/s, and 512 rows 337, 4.8
-// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 455 to 475: issue, 444
-// vector instructions (284 of them to split and decay states) and 44 matrix ones a wavefront and chunk, eight
+// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 490: issue, some 500
+// vector instructions (340 of them to split and decay states) and 56 matrix ones a wavefront and chunk, eight
 // wavefronts a CU.  480 segments of 256 rows of state (65536 tokens, 80 heads) 1120: issue, 333 and 72, at two wavefronts a SIMD.
 #pragma once
 
@@ -73,6 +73,7 @@ template <typename T> struct LinearWalk {
     unsigned* ticket;
     unsigned* done;
     float* handed;
+    bool alone;              // a chain's workgroups have a CU each
 };
 
 // ---- rows and segments ----------------------------------------------------------------------------------
@@ -339,14 +340,14 @@ template <int CH> struct LinearCols<float, CH> {
     __device__ __forceinline__ void load(Vec8<float>& f, int tile, int t) const { d.load(f, stage + tile, t); }
 };
 
-// An fp32 operand whose product keeps all of fp32: three bf16 values, hi + mid + lo, the value to 2^-24 (kThree), or a pair.
-template <typename T, bool kThree> struct LinearExact {
+// An fp32 operand whose product keeps all of fp32: three bf16 values, hi + mid + lo, the value to 2^-24.
+template <typename T> struct LinearExact {
     Pair<T> p;
     Vec8<T> lo;
     __device__ __forceinline__ void set(const float (&v)[8])
     {
         p.set(v);
-        if constexpr (kThree && sizeof(T) == 2) {
+        if constexpr (sizeof(T) == 2) {
             float left[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) left[i] = v[i] - p.hi.get(i) - p.lo.get(i);
@@ -355,16 +356,16 @@ template <typename T, bool kThree> struct LinearExact {
     }
 };
 // a exact and b in T, and the other way round
-template <typename T, bool kThree>
-__device__ __forceinline__ void mma_ex(f32x4& acc, const LinearExact<T, kThree>& a, const Vec8<T>& b)
+template <typename T>
+__device__ __forceinline__ void mma_ex(f32x4& acc, const LinearExact<T>& a, const Vec8<T>& b)
 {
-    if constexpr (kThree && sizeof(T) == 2) mma(acc, a.lo, b);
+    if constexpr (sizeof(T) == 2) mma(acc, a.lo, b);
     mma_px(acc, a.p, b);
 }
-template <typename T, bool kThree>
-__device__ __forceinline__ void mma_xe(f32x4& acc, const Vec8<T>& a, const LinearExact<T, kThree>& b)
+template <typename T>
+__device__ __forceinline__ void mma_xe(f32x4& acc, const Vec8<T>& a, const LinearExact<T>& b)
 {
-    if constexpr (kThree && sizeof(T) == 2) mma(acc, a, b.lo);
+    if constexpr (sizeof(T) == 2) mma(acc, a, b.lo);
     mma_xp(acc, a, b.p);
 }
 
@@ -778,9 +779,8 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
 #pragma unroll
                     for (int m = 0; m < 4; ++m) { s8[m] = st[2 * kb][j][m]; s8[4 + m] = st[2 * kb + 1][j][m]; }
                     if constexpr (kDg) {
-                        // dg is an fp32 sum in which much cancels, and takes its terms from here; most are S''s
-                        LinearExact<T, false> f;
-                        LinearExact<T, true> df;
+                        // dg is an fp32 sum in which much cancels, and takes its terms from here
+                        LinearExact<T> f, df;
                         f.set(s8);
 #pragma unroll
                         for (int m = 0; m < 4; ++m) { s8[m] = dst[2 * kb][j][m]; s8[4 + m] = dst[2 * kb + 1][j][m]; }
@@ -835,10 +835,10 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
 
         // The state behind the chunk is an fp32 result: its weighted values are three bf16 values each, the state then as exact as
         // fp32 sums are (1e-7 to 4e-7 of its norm).  Pairs left 2.4e-6, and where dg cancels up to 3e-5 of that; they take
-        // 2 % off the forward of 320 rows, 10 % off 65536 tokens' with 256 rows of state.  S' adds to dg's terms what
-        // a chunk itself brings, a small part: pairs (dg's error at most 3e-6; with three 1e-6, the backward 3 % longer).
-        LinearExact<T, true> vw[JT];
-        LinearExact<T, false> dvw[kDg ? JT : 1];
+        // 2 % off the forward of 320 rows, 10 % off 65536 tokens' with 256 rows of state.  So are the ones of S' and, where
+        // they are read, both states: dg is then as exact as an fp32 sum; with pairs for S and for what a chunk adds to S'
+        // the backward takes 3 to 4 % less, and dg is 3e-6 off, or in one head of 22 tokens 2.5e-5.
+        LinearExact<T> vw[JT], dvw[kDg ? JT : 1];
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
             float w8[8];
@@ -966,6 +966,9 @@ template <typename T> int64_t walk_blocks(const LinearWalk<T>& p, int columns)
     return linear_items(p.d, p.seg) * p.d.nheads * ((p.Dv + columns - 1) / columns);
 }
 
+// LDS of a launch: more than half of what there is where a second workgroup is not wanted on the CU.
+template <typename T> int walk_lds(const LinearWalk<T>& p, int need) { return p.ticket && p.alone ? std::max(need, 84 * 1024) : need; }
+
 template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg>
 hipError_t launch_walk(const LinearWalk<T>& p, hipStream_t stream)
 {
@@ -974,8 +977,7 @@ hipError_t launch_walk(const LinearWalk<T>& p, hipStream_t stream)
     const int64_t blocks = walk_blocks(p, NW * JT * 16);
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((linear_walk_kernel<T, KB, NW, JT, kBudget, kOut, kDg>), dim3((unsigned)blocks), dim3(NW * 64),
-                       // (a chain's segments one to a CU: one that waits takes no other's turn)
-                       p.ticket ? std::max(S::kLds, 84 * 1024) : S::kLds, stream, p);
+                       walk_lds(p, S::kLds), stream, p);
     return hipGetLastError();
 }
 
@@ -987,7 +989,7 @@ hipError_t launch_twin(const LinearWalk<T>& a, const LinearWalk<T>& b, hipStream
     const int64_t first = walk_blocks(a, 64 * W::JT), blocks = first + walk_blocks(b, 64 * W::JT2);
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL((linear_twin_kernel<T, KB, KB2, kBudget, kOut>), dim3((unsigned)blocks), dim3(256),
-                       a.ticket ? std::max(W::kLds, 84 * 1024) : W::kLds, stream, a, b, (int)first);
+                       walk_lds(a, W::kLds), stream, a, b, (int)first);
     return hipGetLastError();
 }
 

@@ -393,3 +393,17 @@ def test_most_rows_of_one_token():
         # roundings of at most the terms' 2-norm, their signs being random, doubled; rows are added in 64 bits
         size, count = ((D * a * h).square().sum((0, 2, 3)).sqrt().norm(), 64) if n == "dg" else (w.norm(), 33)
         assert (got[n].double() - w).norm() <= 2.0 ** -24 * count ** 0.5 * 2 * size, n
+
+
+@pytest.mark.parametrize("b,L,H,P,N,G", [(1, 22, 1, 64, 240, 1), (5, 32, 8, 16, 128, 4), (7, 1, 14, 48, 160, 14), (4, 393, 10, 64, 32, 2),
+                                         (1, 151, 3, 64, 16, 3), (2, 2048, 150, 16, 48, 150)])
+def test_gradient_of_the_decay_as_in_fp32(b, L, H, P, N, G):
+    """bf16 inputs: what leads to dg keeps 2^-24 of every operand (three bf16 values), so it is off by fp32's roundings, and
+    by as much again for what the three values leave."""
+    import mamba_ssd_sequence_chunked_amd as ssd
+    d = ref.make(b, L, H, P, N, G, "bf16", True, seed=840)
+    got = ssd.linear_backward(*inputs(d), dev(d["dy"], "bf16"), dev(d["init"]), dev(d["dfinal"]))
+    m = H // G
+    want, size = ref.backward(d["v"][:, :, -1:], d["g"][-m:], d["k"][:, :, -1:], d["q"][:, :, -m:], d["dy"][:, :, -m:],
+                              d["init"][:, -m:], d["dfinal"][:, -m:])
+    hold("dg", got["dg"][-m:], want["dg"], size["dg"], 2 * dg_unit("f32", L, N, P) + b * ROUND["f32"])
