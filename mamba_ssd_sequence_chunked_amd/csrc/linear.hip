@@ -199,7 +199,7 @@ hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* 
 //    a row's segments go to whichever CU is free (forward of 320 walks 240 us, whole 274; 384: 264, 282; 640: 442, 513; 768:
 //    525, 558; a backward of three launches of 320: 855, 1056). Not where nearly all CUs have two (448: 330, 305), nor for
 //    fewer tokens than the starts are worth. Two workgroups share a CU from 512 walks on (heads of 64 x 256, 640 walks: 575, alone
-//    683; the backward's two launches together 843, 854); fewer rows do not keep two busy, since segments behind their row's
+//    683; the backward's two launches together 843, 854, then with pairs towards dg); fewer rows do not keep two busy, since segments behind their row's
 //    first one wait (the backward of 160 heads of 128 x 128: 787, not alone 843). As many segments as leave the fewest
 //    CUs idle at the end (288 walks: 2 take 243, 3 229, 4 229; 352: 256, 287, 277; 576: 430, 414, 412). Towards dg, where two on a
 //    CU take as long as one after the other, a CU counts once (the backward of 640: 2 take 1594, 4 1645), and in fp32.
@@ -260,7 +260,7 @@ Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv
 
 // dk's and dv's walks in one launch, where each has a workgroup for all columns: the GPU is filled as by one walk of twice as
 // many rows, what both read is in the XCD's cache for the second, and where rows are cut there are half the launches. The
-// backward of 320 rows of 64 x 128 over 4096 tokens takes 873 us, with two launches 936; of 192 540, 602; of 160 heads of
+// backward of 320 rows of 64 x 128 over 4096 tokens took 873 us when this was done, with two launches 936; of 192 540, 602; of 160 heads of
 // 128 x 128 807, 949; of 12 rows of 32 x 48 over 501 tokens in fp32 57, 77. None of 22 sizes was slower.
 bool walk_twin(const DeltaDims& d, int elem_bytes, Cut& c)
 {

@@ -33,8 +33,8 @@
 // into a chain: one launch in which a segment takes over the state when the one before it is done.
 //
 // What bounds it, and what it takes (bf16, heads of 64 x 128, 4096 tokens): 320 rows 246 us, 4.1 TB/s, and 512 rows 337, 4.8
-// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 490: issue, some 500
-// vector instructions (340 of them to split and decay states) and 56 matrix ones a wavefront and chunk, eight
+// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 530: issue, 519
+// vector instructions (some 340 of them to split and decay states) and 52 matrix ones a wavefront and chunk, eight
 // wavefronts a CU.  480 segments of 256 rows of state (65536 tokens, 80 heads) 1120: issue, 333 and 72, at two wavefronts a SIMD.
 #pragma once
 
