@@ -1,7 +1,7 @@
 // linear_dispatch.hpp - which shape of the walk runs a call (included by the files that instantiate it).
 //
 // bf16: 64 columns of the state a workgroup of four wavefronts, 128 where there are more (two tiles of 16 a wavefront), and
-// as many stages of LDS (two to four) as leave room for a second workgroup on the CU.  fp32: 64 columns, all of LDS.
+// as many stages of LDS (two or three) as leave room for a second workgroup on the CU.  fp32: 64 columns, all of LDS.
 // Towards dg, where the state is twice as large, a wavefront has one tile of 16.
 #pragma once
 

@@ -24,7 +24,7 @@
 // Columns of the state do not mix: a wavefront keeps JT x 16 of them for the whole walk as accumulator tiles (rows Dk,
 // columns Dv), which are operand fragments as they are (see common.hpp).  The chunk's scores are needed by all of them:
 // three make a 16 x 16 tile each, one chunk ahead of the one whose state products run, so that a chunk has one barrier.
-// Copies run two to four stages of LDS ahead.  (Fewer stages, where the rows are wide: the scores are made in their own
+// Copies run into a ring of two or three stages of LDS.  (Fewer stages, where the rows are wide: the scores are made in their own
 // chunk, with a second barrier.)  Chunks have 32 tokens: with 64 the scores are more than what is saved per
 // chunk, and the registers do not hold what is read ahead.
 //
