@@ -65,7 +65,7 @@ __global__ __launch_bounds__(256) void linear_join_kernel(float* __restrict__ lo
                 *reinterpret_cast<f32x4*>(loc + to) = s;
                 if constexpr (kDg) *reinterpret_cast<f32x4*>(dloc + to) = ds;
             }
-            const float a = len == min(seg, n) ? decay.next() : expf(gl * (float)len);
+            const float a = len == min(seg, n) ? decay.next() : linear_power(gl, (float)len);
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 if constexpr (kDg) ds[m] = fmaf(fmaf((float)len, s[m], ds[m]), a, dadd[i][m]);

@@ -212,6 +212,14 @@ __device__ __forceinline__ bool linear_task(const DeltaDims& d, int64_t seg, int
     return false;
 }
 
+// exp(g n) to an ulp or two.  g n is rounded, and an exponent that is off by half a step of up to 64 takes the power off by 64
+// of its own half steps (a token whose successors are zeros had its state 3.5e-6 off); what the rounding took is put back.
+__device__ __forceinline__ float linear_power(float g, float n)
+{
+    const float x = g * n, w = expf(x);
+    return fmaf(w, fmaf(g, n, -x), w);
+}
+
 // A power a^n that a state is multiplied by again and again.  Rounded to fp32 it would be off by the same part every
 // time, which adds up where the decay is slow; so the fp32 neighbours below and above it take turns such that their
 // product stays within one rounding of the power's.
@@ -555,8 +563,8 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
 
     // ---- tables of powers
     const int e = p.back ? 0 : 1;
-    const float a16 = expf(gl * 16.f);
-    const float into0 = expf(gl * (r + e)), into1 = into0 * a16;  // a^(t + e)
+    const float a16 = linear_power(gl, 16.f);
+    const float into0 = linear_power(gl, (float)(r + e)), into1 = into0 * a16;  // a^(t + e)
     // the tile of scores that this wavefront makes: t, s = (0, 0), (1, 0), (1, 1); its weights, and t - s times those
     const int tile_t = wave > 0, tile_s = wave == 2;
     float tilew[4];
@@ -564,7 +572,7 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
 #pragma unroll
     for (int m = 0; m < 4; ++m) {
         const int gap = 16 * (tile_t - tile_s) + r - 4 * g4 - m;
-        tilew[m] = gap >= 0 ? expf(gl * gap) : 0.f;
+        tilew[m] = gap >= 0 ? linear_power(gl, (float)gap) : 0.f;
         tiled[m] = gap > 0 ? tilew[m] * gap : 0.f;
     }
     float outw[8];
@@ -572,7 +580,7 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
     decay.set(gl, kLC);
     auto weights = [&](int rows) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) outw[i] = expf(gl * max(rows - ((i >> 2) * 16 + 4 * g4 + (i & 3)) - e, 0));
+        for (int i = 0; i < 8; ++i) outw[i] = linear_power(gl, (float)max(rows - ((i >> 2) * 16 + 4 * g4 + (i & 3)) - e, 0));
     };
     weights(kLC);
 
@@ -889,7 +897,7 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
                 dvw[j].set(w8);
             }
         }
-        const float a = rows < kLC ? expf(gl * rows) : decay.next();
+        const float a = rows < kLC ? linear_power(gl, (float)rows) : decay.next();
 #pragma unroll
         for (int nt = 0; nt < kNT; ++nt) {
 #pragma unroll
