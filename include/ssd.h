@@ -402,10 +402,14 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  *     65535, nseq <= 2^24, tokens < 2^31. There is no chunk size. Grids limit the sizes too (SSD_ERR_SHAPE): (rows + their
  *     segments) * nheads * the 64-column slices of the wider of headdim and dstate < 2^24, rows * nheads * headdim * dstate
  *     < 2^34, tokens * ngroups * the wider < 2^34; for ssd_linear_step batch * nheads * headdim < 2^28.
- *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too (5e-7 of their norm, dg 2e-6 where its terms
- *     cancel): what leads to them is carried as three bf16 values. bf16 outputs are a little further off than
- *     their own rounding (1.7e-3 of the norm), because the scores and, where they are read, the states are rounded to
- *     bf16 on the way: up to 2.6e-3. With fp32 inputs everything is fp32.
+ *   - Final states, dinit and dg keep fp32's accuracy with bf16 inputs too: what leads to them is carried as three bf16
+ *     values. States and dinit are off by 5e-7 of their norm, dg by 1e-6 of the 2-norm of what its tokens add to it (more of dg
+ *     itself where that cancels). A state is rounded three times with every chunk of 32 tokens, with fp32 inputs with every
+ *     token; where it hardly decays n roundings add up to 2^-24 sqrt(n / 6) of its norm. Measured: states 4e-7 after 2048
+ *     tokens, 1.6e-6 after 65536, with fp32 inputs 8e-7 and 4.7e-6; dg 3.3e-6 after 65536.
+ *   - bf16 outputs are a little further off than their own rounding (1.7e-3 of the norm), because the scores and, where they are
+ *     read, the states are rounded to bf16 on the way: 2.4e-3, at most 2.6e-3. With fp32 inputs everything is fp32: outputs
+ *     are off by 1e-6 of their norm and by what their states are.
  *   - Sums are made in a fixed order: the same call gives the same bits.
  *   - Non-finite inputs: tokens are summed in chunks of 32 (of their sequence or of a segment of it) in which later
  *     tokens have a weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of its chunk and
