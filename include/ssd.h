@@ -415,7 +415,8 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  *     tokens have a weight of zero, so a NaN or Inf at a token can reach the outputs of earlier tokens of its chunk and
  *     all later ones (where the decay has left nothing of it, it need not), of the heads that read it, never another
  *     sequence, batch row or group. dk's and dv's chunks go from the end: there it can reach later tokens of the
- *     chunk and all earlier ones.
+ *     chunk and all earlier ones. What arrives of an Inf is an Inf or a NaN: with bf16 inputs a NaN in the states, as an Inf
+ *     less its bf16 value is, and where it meets a weight or an element of zero.
  * ------------------------------------------------------------------------------------------- */
 
 /* y, final_states over whole sequences.
