@@ -485,8 +485,11 @@ int ssd_linear_step(float* state, const int32_t* slots, int64_t nslots, const vo
  *   states float (nlayers, nslots, slot_floats), read (in place) and written
  *   source float (nlayers, nsource, slot_floats) or NULL (then nsource = nslots): for instance the final states of a prefill
  *   src int32 (nslots), DEVICE memory; any content is safe
- * No workspace. 0 <= nlayers <= 65535; 0 <= nslots <= 65535, in place at most 2048; nsource <= 2^24; slot_floats (nheads *
- * headdim * dstate) a multiple of 4, at most 2^32. The values are copied as they are, NaN included. */
+ * No workspace. 0 <= nlayers <= 65535; 0 <= nslots <= 65535, in place at most 2048, since all that moves is held at once;
+ * nsource <= 2^24; slot_floats (nheads * headdim * dstate) a multiple of 4, at most 2^32. The values are copied as they are, NaN
+ * included. A larger pool moves through a buffer of as many states as move, in two calls: into the buffer with source = the
+ * pool, and back with source = the buffer (-2 for the slots that stay). ssd_step and ssd_delta_step take no slots: they
+ * advance the first `batch` states of a layer, which a pool that is kept compact has its live ones in. */
 int ssd_state_move(float* states, const float* source, const int32_t* src, int64_t nlayers, int64_t nslots,
                    int64_t nsource, int64_t slot_floats, void* stream);
 

@@ -130,7 +130,7 @@ __global__ __launch_bounds__(256) void linear_zero_kernel(unsigned* p, int64_t n
 size_t walk_bytes(const DeltaDims& d, const Cut& c, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
     if (c.seg == kWholeRows) return 0;
-    const int64_t columns = linear_columns(elem_bytes, dg, (int)Dv), walks = d.seqs * d.nheads * ((Dv + columns - 1) / columns);
+    const int64_t columns = linear_columns(elem_bytes, (int)Dv), walks = d.seqs * d.nheads * ((Dv + columns - 1) / columns);
     if (c.chain) return bytes_up(walks + 1) + bytes_up(d.seqs * d.nheads * linear_handed(elem_bytes, dg, Dk, Dv));
     return (dg ? 2 : 1) * bytes_up(state_floats(d, linear_items(d, c.seg)));
 }
@@ -160,7 +160,7 @@ hipError_t walk(LinearWalk<T> (&p)[N], const Cut& c, const float* enter, float* 
     if (c.seg != kWholeRows && c.chain) {
         int64_t words[2] = {0, 0};
         for (int i = 0; i < N; ++i) {
-            const int64_t columns = linear_columns(sizeof(T), kDg, p[i].Dv);
+            const int64_t columns = linear_columns(sizeof(T), p[i].Dv);
             words[i] = d.seqs * d.nheads * ((p[i].Dv + columns - 1) / columns) + 1;
             p[i].ticket = reinterpret_cast<unsigned*>(room[i]);
             p[i].done = p[i].ticket + 1;
@@ -253,7 +253,7 @@ int64_t brief_tokens(int elem_bytes) { return elem_bytes == 2 ? 384 : 192; }
 
 Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
-    const int columns = linear_columns(elem_bytes, dg, (int)Dv);
+    const int columns = linear_columns(elem_bytes, (int)Dv);
     return linear_cut(d, (Dv + columns - 1) / columns, chunk_us(elem_bytes, dg, Dk), least_chunks(elem_bytes),
                       brief_tokens(elem_bytes), dg || elem_bytes == 4);
 }
@@ -265,7 +265,7 @@ Cut walk_cut(const DeltaDims& d, int elem_bytes, bool dg, int64_t Dk, int64_t Dv
 bool walk_twin(const DeltaDims& d, int elem_bytes, Cut& c)
 {
     if (d.headdim > 128 || d.dstate > 128) return false;
-    const int cv = linear_columns(elem_bytes, false, (int)d.headdim), ck = linear_columns(elem_bytes, false, (int)d.dstate);
+    const int cv = linear_columns(elem_bytes, (int)d.headdim), ck = linear_columns(elem_bytes, (int)d.dstate);
     const int64_t slices = (d.headdim + cv - 1) / cv + (d.dstate + ck - 1) / ck;
     c = linear_cut(d, slices, chunk_us(elem_bytes, false, std::max(d.headdim, d.dstate)), least_chunks(elem_bytes),
                    brief_tokens(elem_bytes), elem_bytes == 4);
@@ -290,7 +290,7 @@ GradLayout grad_layout(const DeltaDims& d, int elem_bytes)
     l.twin = walk_twin(d, elem_bytes, both);
     if (l.twin) l.ck = l.cv = both;
     l.items = linear_items(d, l.cq.seg);
-    const int columns = linear_columns(elem_bytes, true, (int)d.dstate);
+    const int columns = linear_columns(elem_bytes, (int)d.dstate);
     l.parts = (int)((d.dstate + columns - 1) / columns) * linear_waves(elem_bytes, true, (int)d.dstate);
     // (walks that run one after another share a room for their states)
     const size_t bk = walk_bytes(d, l.ck, elem_bytes, false, d.headdim, d.dstate),
@@ -318,7 +318,7 @@ int64_t linear_blocks(const DeltaDims& d, int elem_bytes)
     int64_t most = 0;
     for (const bool dg : {false, true})
         for (const int64_t Dv : {d.headdim, d.dstate}) {
-            const int columns = linear_columns(elem_bytes, dg, (int)Dv);
+            const int columns = linear_columns(elem_bytes, (int)Dv);
             most = std::max(most, linear_items(d, walk_cut(d, elem_bytes, dg, d.headdim + d.dstate - Dv, Dv).seg) * d.nheads * ((Dv + columns - 1) / columns) *
                                       (linear_waves(elem_bytes, dg, (int)Dv) > 4 ? 2 : 1));
         }

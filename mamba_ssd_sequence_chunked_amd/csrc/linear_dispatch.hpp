@@ -27,11 +27,11 @@ hipError_t launch_linear_walk(const LinearWalk<T>& p, hipStream_t stream)
 {
     if constexpr (kDg) {
         if constexpr (sizeof(T) == 2)
-            if (linear_columns(sizeof(T), true, p.Dv) == 128) return walk_kb<T, 8, 1, kOut, kDg>(p, stream);
+            if (linear_columns(sizeof(T), p.Dv) == 128) return walk_kb<T, 8, 1, kOut, kDg>(p, stream);
         return walk_kb<T, 4, 1, kOut, kDg>(p, stream);
     } else {
         if constexpr (sizeof(T) == 2)
-            if (linear_columns(sizeof(T), false, p.Dv) == 128) return walk_kb<T, 4, 2, kOut, kDg>(p, stream);
+            if (linear_columns(sizeof(T), p.Dv) == 128) return walk_kb<T, 4, 2, kOut, kDg>(p, stream);
         return walk_kb<T, 4, 1, kOut, kDg>(p, stream);
     }
 }

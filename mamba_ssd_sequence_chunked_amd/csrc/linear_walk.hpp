@@ -318,7 +318,9 @@ template <typename T, int KB, int NW, int JT, int kBudget, bool kOut, bool kDg> 
     static constexpr int kCopies = (kOut ? 2 : 1) * (DTile<CHk>::kInst / NW) + (kHasX ? 2 : 1) * (DTile<CHv>::kInst / NW);
     static constexpr int kStores = kOut ? 2 * JT : 0;
     // wavefronts a SIMD that the registers are shared out for: two, unless the states alone take half of what they would have
-    static constexpr int kWaves = KB * 8 * JT * (kDg ? 2 : 1) <= (sizeof(T) == 2 ? 127 : 63) ? 2 : 1;
+    // (and a workgroup of eight wavefronts puts two on each SIMD in any case)
+    static constexpr int kWaves = NW > 4 || KB * 8 * JT * (kDg ? 2 : 1) <= (sizeof(T) == 2 ? 127 : 63) ? 2 : 1;
+    static_assert(4 * kWaves >= NW, "a workgroup fits a CU");
 };
 
 // Operand fragments of a stage.  What changes with the stage is added to the lane's addresses once a chunk (at), the
@@ -1039,13 +1041,13 @@ hipError_t launch_twin(const LinearWalk<T>& a, const LinearWalk<T>& b, hipStream
 }
 
 // Columns of the state that a workgroup of a walk holds (kDg: of a walk towards dg), and wavefronts it has.
-constexpr int linear_columns(int elem_bytes, bool dg, int Dv) { return elem_bytes == 2 && Dv > 64 ? 128 : 64; }
-constexpr int linear_waves(int elem_bytes, bool dg, int Dv) { return dg ? linear_columns(elem_bytes, dg, Dv) / 16 : 4; }
+constexpr int linear_columns(int elem_bytes, int Dv) { return elem_bytes == 2 && Dv > 64 ? 128 : 64; }
+constexpr int linear_waves(int elem_bytes, bool dg, int Dv) { return dg ? linear_columns(elem_bytes, Dv) / 16 : 4; }
 
 // Floats of the state that a walk hands on (kDg: of both), its rows and columns rounded up to what a workgroup holds.
 constexpr int64_t linear_handed(int elem_bytes, bool dg, int64_t Dk, int64_t Dv)
 {
-    const int64_t rows = Dk <= 32 ? 32 : Dk <= 64 ? 64 : Dk <= 128 ? 128 : 256, columns = linear_columns(elem_bytes, dg, (int)Dv);
+    const int64_t rows = Dk <= 32 ? 32 : Dk <= 64 ? 64 : Dk <= 128 ? 128 : 256, columns = linear_columns(elem_bytes, (int)Dv);
     return (dg ? 2 : 1) * rows * ((Dv + columns - 1) / columns * columns);
 }
 

@@ -584,7 +584,8 @@ def linear_forward_varlen(v: torch.Tensor, g: torch.Tensor, k: torch.Tensor, q: 
 
     v (T, ngroups, headdim); g (nheads,) fp32; k (T, ngroups, dstate), q (T, nheads, dstate) in v's dtype; cu_seqlens
     int32 (nseq + 1,) on the same device; init_states (nseq, nheads, headdim, dstate) fp32 or None.
-    Returns (y (T, nheads, headdim) in v's dtype, final_states (nseq, nheads, headdim, dstate))."""
+    Returns (y (T, nheads, headdim) in v's dtype, final_states (nseq, nheads, headdim, dstate)); y of tokens behind
+    cu_seqlens[nseq] is not set."""
     lib = load_library()
     if v.dim() != 3 or q.dim() != 3:
         raise ValueError("v must be (T, ngroups, headdim) and q (T, nheads, dstate)")
@@ -683,7 +684,8 @@ def state_move(states: torch.Tensor, src: torch.Tensor, source: Optional[torch.T
 
     states (nslots, nheads, headdim, dstate) or (nlayers, nslots, nheads, headdim, dstate) fp32, changed in place and
     returned; src int32 (nslots,): slot i becomes source[src[i]], zeros where src[i] is -1, and stays otherwise.  source:
-    another pool of the same layers and state sizes, or None: the pool itself, as it was before the call."""
+    another pool of the same layers and state sizes, or None: the pool itself, as it was before the call (then at most 2048
+    slots: a larger pool moves through a buffer, in two calls)."""
     lib = load_library()
     if states.dim() not in (4, 5):
         raise ValueError("states must be ([nlayers,] nslots, nheads, headdim, dstate)")

@@ -27,3 +27,25 @@ def test_inf_is_confined(where, dt):
         assert torch.equal(y0[..., rest], y1[..., rest]) and torch.equal(f0[:, :, rest], f1[:, :, rest])
     else:
         assert not y1[0, 130:, 2:].isfinite().any() and not f1[0, 2:, :, 5].isfinite().any()
+
+
+def test_a_pool_too_large_to_move_in_place():
+    """More than 2048 slots are refused in place and move through a buffer, in two calls: what the header says."""
+    import torch
+    import mamba_ssd_sequence_chunked_amd as ssd
+    n, H, P, N = 4000, 2, 16, 16
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    pool = torch.randn((2, n, H, P, N), generator=gen, device="cuda")
+    old = pool.clone()
+    table = lambda t: torch.tensor(t, dtype=torch.int32, device="cuda")      # noqa: E731
+    with pytest.raises(ssd.SSDError):
+        ssd.state_move(pool, torch.arange(n, dtype=torch.int32, device="cuda"))
+    into, take = [3990, 17, 5, 2500, 6], [17, 3990, 3999, 17, 17]             # two change places, one moves down, two forks
+    buffer = torch.empty((2, len(take), H, P, N), device="cuda")
+    ssd.state_move(buffer, table(take), source=pool)
+    src = torch.full((n,), -2, dtype=torch.int32, device="cuda")
+    src[into], src[3999] = table(range(len(take))), -1
+    ssd.state_move(pool, src, source=buffer)
+    want = old.clone()
+    want[:, into], want[:, 3999] = old[:, take], 0
+    assert torch.equal(pool, want)
