@@ -2,7 +2,9 @@
 //
 // bf16: 64 columns of the state a workgroup of four wavefronts, 128 where there are more (two tiles of 16 a wavefront), and
 // as many stages of LDS (two or three) as leave room for a second workgroup on the CU.  fp32: 64 columns, all of LDS.
-// Towards dg, where the state is twice as large, a wavefront has one tile of 16.
+// Towards dg, where the state is twice as large, a wavefront has one tile of 16, and a workgroup of 128 columns eight wavefronts.
+// With more than 128 rows those have 69 registers a lane in scratch (4 x 4096 tokens, 16 heads of 256 x 128: the backward takes 1023
+// us, with four wavefronts and 64 columns, which spill none, 924); the fp32 walk of as many rows has 75.
 #pragma once
 
 #include "linear_walk.hpp"

@@ -33,9 +33,11 @@
 // into a chain: one launch in which a segment takes over the state when the one before it is done.
 //
 // What bounds it, and what it takes (bf16, heads of 64 x 128, 4096 tokens): 320 rows 246 us, 4.1 TB/s, and 512 rows 337, 4.8
-// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 530: issue, 519
+// TB/s, where a copy reaches 4.83: HBM, once the CUs are filled evenly.  320 rows towards dq and dg 520: issue, 521
 // vector instructions (some 340 of them to split and decay states) and 52 matrix ones a wavefront and chunk, eight
-// wavefronts a CU.  480 segments of 256 rows of state (65536 tokens, 80 heads) 1120: issue, 333 and 72, at two wavefronts a SIMD.
+// wavefronts a CU.  480 segments of 256 rows of state (65536 tokens, 80 heads) 1120: issue, 333 and 72, at two wavefronts a
+// SIMD, and LDS, 98 of whose 335 cycles a chunk are bank conflicts (see LinearRows).  In fp32 320 rows take 716, the matrix
+// products at 58 % of the rate of a large one, with a workgroup a CU.
 #pragma once
 
 #include <algorithm>
@@ -332,7 +334,8 @@ template <int CH> struct LinearRows<bf16, CH> {
     unsigned b[2][kPer][2];
     __device__ __forceinline__ LinearRows(int r, int g) : d(r, g) {}
     // (rows 16 on have addresses of their own: from one, the compiler would read both rows' quads in one instruction, and
-    // move them to their fragments after)
+    // move them to their fragments after.  Where a row has 256 elements it still joins blocks kb and kb + 4, 256 bytes apart, in
+    // the scores' reads; the halves of such a read fall on the same banks)
     __device__ __forceinline__ void at(unsigned stage)
     {
 #pragma unroll
@@ -733,6 +736,9 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
         }
 #pragma unroll
         for (int m = 0; m < 4; ++m) sc[m] *= tilew[m];
+        // With bf16 inputs decayed scores are rounded to bf16, and so is the state where outputs are read from it: bf16 outputs are
+        // 2.35e-3 of their norm off, 1.66e-3 of it their own rounding.  As pairs both would leave that alone; 320 rows then take
+        // 286 us, now 250, 65536 tokens 1738, now 1520, the backward of 320 rows 932, now 880.
         // tile (0, 0) alone, then (1, 0) and (1, 1) side by side
         lds_put(to_lds + (wave == 0 ? lane * 4 * S::kEs : (256 + lane * 8 + tile_s * 4) * S::kEs), sc, T());
     };
@@ -838,7 +844,7 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
                             mma_ex(dacc[t][j], df, qf[kb & 1][t]);
                         }
                     } else {
-                        Vec8<T> f;
+                        Vec8<T> f;                                 // (rounded to bf16: see make_scores)
                         pack8(f, s8);
 #pragma unroll
                         for (int t = 0; t < 2; ++t) mma(acc[t][j], f, qf[kb & 1][t]);
@@ -881,10 +887,10 @@ __device__ __forceinline__ void linear_walk_run(const LinearWalk<T>& p, int bloc
         }
 
         // The state behind the chunk is an fp32 result: its weighted values are three bf16 values each, the state then as exact as
-        // fp32 sums are (1e-7 to 4e-7 of its norm).  Pairs left 2.4e-6, and where dg cancels up to 3e-5 of that; they take
-        // 2 % off the forward of 320 rows, 10 % off 65536 tokens' with 256 rows of state.  So are the ones of S' and, where
-        // they are read, both states: dg is then as exact as an fp32 sum; with pairs for S and for what a chunk adds to S'
-        // the backward takes 3 to 4 % less, and dg is 3e-6 off, or in one head of 22 tokens 2.5e-5.
+        // fp32 sums are (4e-8 to 4e-7 of its norm).  Pairs left 2.4e-6, and where dg cancels up to 3e-5 of that; they take
+        // 2 % off the forward of 320 rows and its backward, 9 % off 65536 tokens' with 256 rows of state.  So are the ones of S'
+        // and, where they are read, both states: dg is then as exact as an fp32 sum; with pairs for S and for what a chunk adds
+        // to S' the backward takes 4 to 6 % less, and dg is 3e-6 off, or in one head of 22 tokens 2.5e-5.
         LinearExact<T> vw[JT], dvw[kDg ? JT : 1];
 #pragma unroll
         for (int j = 0; j < JT; ++j) {
