@@ -426,7 +426,7 @@ int ssd_delta_step(float* state, const void* v, const float* g, const float* bet
  *   y T (batch, seqlen, nheads, headdim), written; final_states float (batch, nheads, headdim, dstate), written: the state
  *     after the last token (the initial one when seqlen = 0)
  *   workspace of at least ssd_linear_forward_workspace_bytes() bytes (0 = the sizes or dtype are refused): the states
- *     between segments where few long rows are cut into segments, else 256 */
+ *     between segments where rows are cut into segments, else 256 */
 size_t ssd_linear_forward_workspace_bytes(int64_t batch, int64_t seqlen, int64_t nheads, int64_t headdim,
                                           int64_t dstate, int64_t ngroups, int dtype);
 int ssd_linear_forward(const void* v, const float* g, const void* k, const void* q, const float* init_states, void* y,
@@ -436,7 +436,7 @@ int ssd_linear_forward(const void* v, const float* g, const void* k, const void*
 /* The same for a packed variable-length batch: sequence i is tokens cu_seqlens[i] .. cu_seqlens[i + 1] - 1 of one token
  * axis; a sequence may continue from a state.
  *   v T (total_tokens, ngroups, headdim); k T (total_tokens, ngroups, dstate); q T (total_tokens, nheads, dstate)
- *   cu_seqlens int32 (nseq + 1), DEVICE memory, non-decreasing from 0 to total_tokens (empty sequences
+ *   cu_seqlens int32 (nseq + 1), DEVICE memory, non-decreasing from 0 to at most total_tokens (empty sequences
  *     allowed); content not checked, other content yields unspecified values but no access outside the buffers. Tokens
  *     behind cu_seqlens[nseq] are no sequence's: their y is left as it was
  *   init_states float (nseq, nheads, headdim, dstate) or NULL (zeros)
